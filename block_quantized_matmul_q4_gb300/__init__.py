@@ -57,6 +57,13 @@ _SIGS = {
     "qmm_w4a16": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp]),
     "qmm_w4a16_lut": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp]),
     "qmm_w4a16_unpack_zeros": (_i32, [_vp, _vp, _i64, _i64, _vp]),
+    "qmm_kv_append": (_i32, [_vp, _vp, _vp, _i32, _vp, _i64, _vp, _i64, _i64, _vp]),
+    "qmm_kv_read": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _vp]),
+    "qmm_kv_attention_workspace_bytes": (_sz, [_vp, _i32, _i32, _i64, _i64, _i64]),
+    "qmm_kv_attention": (_i32, [_vp, _vp, _vp, _i32, _vp, _i64, _i64, _i32, ctypes.c_float, _i32, _i64, _i64, _i64,
+                                _vp, _vp, _vp, _sz, _vp]),
+    "qmm_logprobs_workspace_bytes": (_sz, [_i64, _i64, _i32]),
+    "qmm_logprobs": (_i32, [_i32, _vp, _i64, _i64, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "qmm_debug_wait_timeout": (_i32, [_i64, _vp]),
     "qmm_debug_peak": (_i32, [_i32, _i64, ctypes.POINTER(ctypes.c_double), _vp]),
     "qmm_status_string": (ctypes.c_char_p, [_i32]),
@@ -240,6 +247,146 @@ def qmm_w4a16_unpack_zeros(zeros_packed, zeros, N: int, ngroups: int, stream=Non
     ([N, ceil(ngroups/8)]); see include/qmm.h."""
     _check("qmm_w4a16_unpack_zeros",
            _lib.qmm_w4a16_unpack_zeros(_ptr(zeros_packed), _ptr(zeros), N, ngroups, _stream(stream)))
+
+
+# ---------------------------------------------------------------- serving
+QMM_F32, QMM_F16, QMM_BF16 = 0, 1, 2
+_FTYPE = {torch.float32: QMM_F32, torch.float16: QMM_F16, torch.bfloat16: QMM_BF16}
+
+
+def _ftype(t) -> int:
+    if t.dtype not in _FTYPE:
+        raise ValueError(f"float32, float16 or bfloat16 tensor expected, got {t.dtype}")
+    return _FTYPE[t.dtype]
+
+
+def _typed(t, dtype, what: str):
+    if t is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    return _ptr(t)
+
+
+def _heads(t, dim: int, what: str):
+    """(pointer, row stride) of [rows][heads][dim] rows whose heads are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("libqmm takes device tensors")
+    if t.dim() != 3 or t.size(2) != dim or (t.numel() and (t.stride(2) != 1 or (t.size(1) > 1 and t.stride(1) != dim))):
+        raise ValueError(f"{what} must be [rows][heads][{dim}] with contiguous heads")
+    return t.data_ptr(), t.stride(0) if t.size(0) > 1 else max(t.stride(0), t.size(1) * dim)
+
+
+class KvCache(ctypes.Structure):
+    """qmm_kv_cache over tensors: codes k, v int8 [pages][heads][page_tokens][head_dim],
+    scales fp32 [pages][heads]. The tensors are kept alive."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_pages", _i64), ("heads", _i32),
+                ("page_tokens", _i32), ("head_dim", _i32)]
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if k.dim() != 4 or v.shape != k.shape or k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2]:
+            raise ValueError("k and v must be [pages][heads][page_tokens][head_dim], the scales [pages][heads]")
+        super().__init__(_typed(k, torch.int8, "k"), _typed(v, torch.int8, "v"), _typed(k_scale, torch.float32, "k_scale"),
+                         _typed(v_scale, torch.float32, "v_scale"), *k.shape)
+        self.tensors = (k, v, k_scale, v_scale)
+
+
+class KvBatch(ctypes.Structure):
+    """qmm_kv_batch over int32 tensors: table [batch][max_pages], first [batch + 1], length [batch]."""
+    _fields_ = [("table", _vp), ("first", _vp), ("length", _vp), ("batch", _i32), ("max_pages", _i32)]
+
+    def __init__(self, table, first, length):
+        if table.dim() != 2 or first.shape != (table.size(0) + 1,) or length.shape != (table.size(0),):
+            raise ValueError("table must be [batch][max_pages], first [batch + 1], length [batch]")
+        super().__init__(_typed(table, torch.int32, "table"), _typed(first, torch.int32, "first"),
+                         _typed(length, torch.int32, "length"), *table.shape)
+        self.tensors = (table, first, length)
+
+
+class Rope(ctypes.Structure):
+    """qmm_rope over an fp32 tensor [positions][dim / 2][2] of (cos, sin)."""
+    _fields_ = [("table", _vp), ("rows", _i64), ("dim", _i32), ("adjacent", _i32)]
+
+    def __init__(self, table, adjacent: bool = False):
+        if table.dim() != 3 or table.size(2) != 2:
+            raise ValueError("table must be [positions][dim / 2][2]")
+        super().__init__(_typed(table, torch.float32, "table"), table.size(0), 2 * table.size(1), int(adjacent))
+        self.tensors = (table,)
+
+
+def _ref(s):
+    return None if s is None else ctypes.addressof(s)
+
+
+def empty_kv_cache(num_pages: int, heads: int, page_tokens: int, head_dim: int, device="cuda") -> KvCache:
+    shape = (num_pages, heads, page_tokens, head_dim)
+    return KvCache(torch.empty(shape, dtype=torch.int8, device=device), torch.empty(shape, dtype=torch.int8, device=device),
+                   torch.empty(shape[:2], device=device), torch.empty(shape[:2], device=device))
+
+
+def qmm_kv_append(cache: KvCache, batch: KvBatch, rope, K, V, stream=None):
+    """Rows K, V [T][heads][head_dim] (their heads contiguous) into the cache, K
+    rotated by `rope` (a Rope or None) on the way; see include/qmm.h."""
+    k, ks = _heads(K, cache.head_dim, "K")
+    v, vs = _heads(V, cache.head_dim, "V")
+    if V.shape != K.shape or V.dtype != K.dtype or K.size(1) != cache.heads:
+        raise ValueError("K and V must have one type, the same rows and the cache's heads")
+    _check("qmm_kv_append",
+           _lib.qmm_kv_append(_ref(cache), _ref(batch), _ref(rope), _ftype(K), k, ks, v, vs, K.size(0), _stream(stream)))
+
+
+def qmm_kv_read(cache: KvCache, pages, K, V, stream=None):
+    """K, V [n][heads][page_tokens][head_dim]: the values that the n pages hold."""
+    shape = (pages.numel(), cache.heads, cache.page_tokens, cache.head_dim)
+    if K.shape != shape or V.shape != shape or K.dtype != V.dtype:
+        raise ValueError(f"K and V must be {shape} of one type")
+    _check("qmm_kv_read",
+           _lib.qmm_kv_read(_ref(cache), _typed(pages, torch.int32, "pages"), shape[0], _ftype(K), _ptr(K), _ptr(V),
+                            _stream(stream)))
+
+
+def qmm_kv_attention_workspace_bytes(cache: KvCache, batch: int, q_heads: int, T: int, max_q: int, max_kv: int) -> int:
+    return int(_lib.qmm_kv_attention_workspace_bytes(_ref(cache), batch, q_heads, T, max_q, max_kv))
+
+
+def qmm_kv_attention(cache: KvCache, batch: KvBatch, rope, Q, out, lse=None, *, scale: float, causal: bool = True,
+                     window: int = 0, max_q: int, max_kv: int, workspace=None, ws_bytes: int = 0, stream=None):
+    """out [T][q_heads][head_dim] = attention of the rows Q over the cache, lse
+    [T][q_heads] their log sums; max_q and max_kv are the most rows and the
+    largest length of any sequence; see include/qmm.h."""
+    q, stride = _heads(Q, cache.head_dim, "Q")
+    if out.shape != Q.shape or out.dtype != Q.dtype or (lse is not None and lse.shape != Q.shape[:2]):
+        raise ValueError("out must be like Q, lse [rows][q_heads]")
+    _check("qmm_kv_attention",
+           _lib.qmm_kv_attention(_ref(cache), _ref(batch), _ref(rope), _ftype(Q), q, stride, Q.size(0), Q.size(1), scale,
+                                 int(causal), window, max_q, max_kv, _ptr(out), _typed(lse, torch.float32, "lse"),
+                                 _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def qmm_logprobs_workspace_bytes(M: int, V: int, top: int) -> int:
+    return int(_lib.qmm_logprobs_workspace_bytes(M, V, top))
+
+
+def qmm_logprobs(X, given=None, lse=None, entropy=None, given_logp=None, top_ids=None, top_logp=None, workspace=None,
+                 ws_bytes: int = 0, stream=None):
+    """From logits X [M][V] (contiguous within a row): lse and entropy [M],
+    given_logp [M][G] of the ids given [M][G], the most likely top_ids and
+    their top_logp [M][top]; None where not wanted; see include/qmm.h."""
+    if not X.is_cuda:
+        raise ValueError("libqmm takes device tensors")
+    if X.dim() != 2 or (X.size(1) > 1 and X.stride(1) != 1):
+        raise ValueError("X must be [M][V] with contiguous rows")
+    M, V = X.shape
+    G = 0 if given is None else given.numel() // M if M else 0
+    top = 0 if top_ids is None else top_ids.numel() // M if M else 0
+    for t, n, what in ((given, G, "given"), (given_logp, G, "given_logp"), (top_ids, top, "top_ids"), (top_logp, top, "top_logp"),
+                       (lse, 1, "lse"), (entropy, 1, "entropy")):
+        if t is not None and t.numel() != M * n:
+            raise ValueError(f"{what} must hold {n} values for each of the {M} rows")
+    _check("qmm_logprobs",
+           _lib.qmm_logprobs(_ftype(X), X.data_ptr(), X.stride(0) if M > 1 else max(X.stride(0), V), M, V,
+                             _typed(given, torch.int32, "given"), G, top, _typed(lse, torch.float32, "lse"),
+                             _typed(entropy, torch.float32, "entropy"), _typed(given_logp, torch.float32, "given_logp"),
+                             _typed(top_ids, torch.int32, "top_ids"), _typed(top_logp, torch.float32, "top_logp"),
+                             _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 QMM_PEAK_MMA_S8, QMM_PEAK_MMA_F16, QMM_PEAK_TC_SS_128, QMM_PEAK_TC_TS_128, QMM_PEAK_TC_SS_256, \

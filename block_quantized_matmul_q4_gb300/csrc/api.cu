@@ -14,7 +14,8 @@
 namespace qmm {
 
 // Device error word: bit kDevErrTimeout is set by a kernel that gave up a
-// bounded wait. Read and cleared by qmm_check_device_error.
+// bounded wait, kDevErrRange by one that met an offset outside its array.
+// Read and cleared by qmm_check_device_error.
 __device__ unsigned g_device_error = 0;
 
 namespace {
@@ -75,6 +76,24 @@ qmm_status set_error(qmm_status s, const char *fmt, ...) {
     return s;
 }
 
+// Default mem pool: keep freed workspace instead of returning it to the
+// driver at every synchronization. Skipped while `s` is being captured (a
+// pool attribute change would end the capture; allocations in a graph come
+// from the graph's own memory anyway) and done by the next call outside one.
+void prepare_pool(cudaStream_t s) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone) return;
+    const int d = current_device();
+    std::lock_guard<std::mutex> lk(g_mutex);
+    if (g_pool_ready[d]) return;
+    cudaMemPool_t pool;
+    if (cudaDeviceGetDefaultMemPool(&pool, d) == cudaSuccess) {
+        uint64_t thr = UINT64_MAX;
+        cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &thr);
+    }
+    g_pool_ready[d] = true;
+}
+
 namespace {
 
 bool is_weight(qmm_type t) { return t == QMM_TYPE_Q4_0 || t == QMM_TYPE_Q4_K || t == QMM_TYPE_Q6_K; }
@@ -106,24 +125,6 @@ qmm_status check_weight_args(qmm_type wt, int64_t N, int64_t K) {
                   (long long)K, elems(wt));
     QMM_CHECK_ARG(K <= (int64_t)1 << 30 && N <= (int64_t)1 << 31, "sizes too large");
     return QMM_OK;
-}
-
-// Default mem pool: keep freed workspace instead of returning it to the
-// driver at every synchronization. Skipped while `s` is being captured (a
-// pool attribute change would end the capture; allocations in a graph come
-// from the graph's own memory anyway) and done by the next call outside one.
-void prepare_pool(cudaStream_t s) {
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone) return;
-    const int d = current_device();
-    std::lock_guard<std::mutex> lk(g_mutex);
-    if (g_pool_ready[d]) return;
-    cudaMemPool_t pool;
-    if (cudaDeviceGetDefaultMemPool(&pool, d) == cudaSuccess) {
-        uint64_t thr = UINT64_MAX;
-        cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &thr);
-    }
-    g_pool_ready[d] = true;
 }
 
 // More than 16 tokens run the fp16-operand tensor-core GEMM on fp16(2^e d_a y)
@@ -699,6 +700,8 @@ qmm_status qmm_check_device_error(qmm_stream_t stream) {
     }
     if (v & kDevErrTimeout)
         return set_error(QMM_ERR_TIMEOUT, "a kernel gave up a bounded device-side wait");
+    if (v & kDevErrRange)
+        return set_error(QMM_ERR_ARG, "a row offset, length or page id in device memory is outside its array");
     return ok();
 }
 

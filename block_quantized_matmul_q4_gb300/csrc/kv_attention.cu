@@ -1,0 +1,508 @@
+// kv_attention.cu -- attention over the paged 8-bit cache for few rows per
+// sequence (decode steps, short continuations), and the split of a long cache
+// over CTAs.
+//
+// A row's scores are x_j = q . k_j ks_j (in log2 units, the page scale ks
+// constant over a page). Values carry a page scale too, v_j = vs_j c_j, which
+// moves into the exponent: with u_j = x_j + log2 vs_j and any reference m,
+//   w_j = 2^(u_j - m),   out = sum_j w_j c_j / l,   l = sum_j w_j / vs_j,
+//   lse = (m + log2 l) ln 2,
+// so codes enter the tensor cores as they are (|code| <= 128 is exact in
+// fp16) and a page costs one fused multiply-add per score, no product per
+// value. References differ between the parts of a sequence that warps and
+// CTAs take; parts join by scaling with 2^(m_part - m).
+//
+// The rows of all query heads that share a cached head (times the new tokens)
+// form the tile: S^T = K Q^T and O^T = V^T P^T, so that the cache is the
+// 16-row operand and eight rows fill an mma.sync m16n8k16. What bounds a
+// decode step is reading the cache once; the MMAs run at a few percent of
+// their rate, which leaves room for exactness: Q and P are each two fp16
+// numbers (22 bits).
+#include "serving.cuh"
+
+namespace qmm {
+namespace serving {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kStep = 16;        // tokens of a warp's step: one MMA tile of the cache
+constexpr int kPageBlock = 256;  // pages whose ids and scales are staged at once
+constexpr int kSplitTokens = kWarps * kStep;  // split boundaries
+// References: a new one gives its largest score the weight 2^11, and it is
+// renewed when a weight passes 2^15. fp16 holds weights up to 65504, so small
+// ones keep the most bits: two numbers resolve 2^-25, 2^-36 of the largest.
+constexpr float kTop = 11.0f, kRenew = 15.0f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit elements, two of a row per lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// Bytes 0 and 2 of x, signed codes, as two exact fp16 numbers: byte ^ 0x80
+// under the exponent of 1024 is 1152 + code.
+__device__ __forceinline__ uint32_t codes_02(uint32_t x) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(x), "r"(0x00FF00FFu), "r"(0x64806480u));  // (x & m) ^ c
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(d) : "r"(0x64806480u));
+    return d;
+}
+__device__ __forceinline__ uint32_t half_pair(float a, float b) { return pack_pair(QMM_F16, a, b); }
+// a and b less what half_pair(a, b) = h holds of them, as fp16.
+__device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return half_pair(a - f.x, b - f.y);
+}
+
+// Bytes of a head that one lane loads, as the widest loads their alignment allows.
+template <int WORDS>
+__device__ __forceinline__ void load_words(const int8_t *p, uint32_t *w) {
+    if (WORDS % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < WORDS / 4; ++i) {
+            const uint4 u = ld128(p + 16 * i);
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        }
+    } else if (WORDS % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < WORDS / 2; ++i) {
+            const uint2 u = ld64(p + 8 * i);
+            w[2 * i] = u.x, w[2 * i + 1] = u.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = ld32(p + 4 * i);
+    }
+}
+
+// The rows of one work unit and the tokens that any of them sees.
+struct Tile {
+    Seq s;
+    int b, r0, rows;       // rows r0 .. r0 + rows - 1 of the sequence's n * group
+    int start;             // position of the sequence's first row
+    int lo, hi;            // tokens, lo a multiple of 16
+};
+__device__ __forceinline__ Tile tile_of(const Batch &g, const Attend &a, int page, int group, int tile_rows, int64_t unit) {
+    Tile t;
+    const Unit u = find_unit(unit, g.batch, [&](int b) { return (seq_at(g, b, page).n * group + tile_rows - 1) / tile_rows; });
+    t.b = u.b;
+    if (u.b < 0) return t;
+    t.s = seq_at(g, u.b, page);
+    t.r0 = u.i * tile_rows;
+    t.rows = min(tile_rows, t.s.n * group - t.r0);
+    t.start = t.s.len - t.s.n;
+    const int first = t.start + t.r0 / group, last = t.start + (t.r0 + t.rows - 1) / group;
+    t.hi = a.causal ? last + 1 : t.s.len;
+    t.lo = a.window && a.window <= first ? (int)(first - a.window + 1) & ~15 : 0;
+    return t;
+}
+// Splits of a tile's tokens: each `chunk` tokens, the last one the rest.
+__device__ __forceinline__ int splits_of(const Tile &t, int chunk, int splits) {
+    return max(1, min(splits, (t.hi - t.lo + chunk - 1) / chunk));
+}
+
+// Writes a row's result from its joined sums: o / l and the log sum.
+__device__ __forceinline__ void write_lse(const Attend &a, int64_t at, float m, float l) {
+    if (a.lse) a.lse[at] = l == 0.0f ? __int_as_float(0xFF800000) : (m + log2f(l)) * 0.693147180559945f;
+}
+__device__ __forceinline__ void write_out(const Attend &a, int64_t at, float4 o, float l) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (a.ft == QMM_F32)
+        store4<QMM_F32>(a.out, at, o);
+    else if (a.ft == QMM_F16)
+        store4<QMM_F16>(a.out, at, o);
+    else
+        store4<QMM_BF16>(a.out, at, o);
+}
+
+// Shared memory: the staged pages, then rotated Q (fp32), whose place the
+// warps' results take at the end.
+template <int D, int NT>
+struct Smem {
+    int id[kPageBlock];
+    float ks[kPageBlock], lv[kPageBlock], iv[kPageBlock];  // K scale, log2 and inverse of the V scale
+    float ml[2][kWarps][8 * NT];
+    float o[kWarps][8 * NT][D + 4];
+};
+
+// grid: (units of 8 * NT rows, cached heads, splits).
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads)
+    kv_attention_kernel(const Cache c, const Batch g, const Rope rope, const Attend a, int chunk, float *part) {
+    constexpr int kRows = 8 * NT;
+    constexpr int kSteps = D / 16;  // k steps of Q K^T, and 16-row tiles of V^T
+    constexpr int kKWords = D % 64 == 0 ? 4 : 2, kKChunks = D / (16 * kKWords);  // a lane's loads of a K row
+    constexpr int kVWords = D / 32;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    auto &sm = *reinterpret_cast<Smem<D, NT> *>(smem_raw);
+    pdl_launch_dependents();
+    pdl_wait();
+    const int h = blockIdx.y, group = a.q_heads / c.heads;
+    const Tile t = tile_of(g, a, c.page, group, kRows, blockIdx.x);
+    if (t.b < 0) return;
+    const int splits = splits_of(t, chunk, gridDim.z);
+    if ((int)blockIdx.z >= splits) return;
+    const int begin = t.lo + (int)blockIdx.z * chunk;
+    const int end = (int)blockIdx.z == splits - 1 ? t.hi : min(t.hi, begin + chunk);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
+
+    // rotated Q, zeros for rows past the tile
+    float(*qs)[D + 4] = sm.o[0];
+    for (int i = threadIdx.x; i < kRows * (D / 8); i += kThreads) {
+        const int r = i / (D / 8), j = i - r * (D / 8);
+        const int2 q = quad_at(rope, j);
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
+        if (r < t.rows) {
+            const int row = (t.r0 + r) / group, head = h * group + (t.r0 + r) % group;
+            const int64_t at = (int64_t)(t.s.row0 + row) * a.Q.stride + (int64_t)head * D;
+            if (a.ft == QMM_F32) {
+                x = load4<QMM_F32>(a.Q.p, at + q.x), y = load4<QMM_F32>(a.Q.p, at + q.y);
+            } else if (a.ft == QMM_F16) {
+                x = load4<QMM_F16>(a.Q.p, at + q.x), y = load4<QMM_F16>(a.Q.p, at + q.y);
+            } else {
+                x = load4<QMM_BF16>(a.Q.p, at + q.x), y = load4<QMM_BF16>(a.Q.p, at + q.y);
+            }
+            rotate_item(rope, j, t.start + row, x, y);
+        }
+        *reinterpret_cast<float4 *>(&qs[r][q.x]) = x;
+        *reinterpret_cast<float4 *>(&qs[r][q.y]) = y;
+    }
+    __syncthreads();
+
+    // Q as the B operand: lane (lg, lt) holds row lg, and of k step s the four
+    // elements that its K words hold, (0, 2) and (1, 3) paired as codes_02
+    // pairs them. Each row times a power of two that puts its largest
+    // element in [2^13, 2^14).
+    uint32_t qh[NT][kSteps][2], ql[NT][kSteps][2];
+    float qf[NT][2];  // rows 2 lt, 2 lt + 1 of a tile: what undoes that, times the scale
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const float4 v = *reinterpret_cast<const float4 *>(&qs[8 * n + lg][16 * kKWords * (s / kKWords) + 4 * kKWords * lt + 4 * (s % kKWords)]);
+            most = max(max(most, __float_as_uint(v.x) & 0x7FFFFFFFu), __float_as_uint(v.y) & 0x7FFFFFFFu);
+            most = max(max(most, __float_as_uint(v.z) & 0x7FFFFFFFu), __float_as_uint(v.w) & 0x7FFFFFFFu);
+        }
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        // 2^(13 - floor(log2 most)), within fp32's normal numbers; 1 for 0 and non-finite rows
+        const int e = (int)(most >> 23);
+        const int be = e == 0 || e == 255 ? 127 : min(127 + 13 + 127 - e, 253);
+        const float up = __int_as_float(be << 23), down = __int_as_float((254 - be) << 23);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const float4 v = *reinterpret_cast<const float4 *>(&qs[8 * n + lg][16 * kKWords * (s / kKWords) + 4 * kKWords * lt + 4 * (s % kKWords)]);
+            qh[n][s][0] = half_pair(v.x * up, v.z * up);
+            ql[n][s][0] = rest_pair(v.x * up, v.z * up, qh[n][s][0]);
+            qh[n][s][1] = half_pair(v.y * up, v.w * up);
+            ql[n][s][1] = rest_pair(v.y * up, v.w * up, qh[n][s][1]);
+        }
+        qf[n][0] = __shfl_sync(0xffffffffu, down, 8 * lt) * a.scale;
+        qf[n][1] = __shfl_sync(0xffffffffu, down, 8 * lt + 4) * a.scale;
+    }
+    // tokens that rows 2 lt, 2 lt + 1 of a tile see
+    int from[NT][2], to[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 8 * n + 2 * lt + i, pos = t.start + (t.r0 + r) / group;
+            from[n][i] = a.window && a.window <= pos ? (int)(pos - a.window + 1) : 0;
+            to[n][i] = r >= t.rows ? 0 : a.causal ? pos + 1 : t.s.len;
+        }
+
+    const float inf = __int_as_float(0x7F800000);
+    float o[NT][kSteps][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -inf;
+        l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) o[n][s][0] = o[n][s][1] = o[n][s][2] = o[n][s][3] = 0.0f;
+    }
+
+    const int shift = 31 - __clz(c.page);
+    for (int b0 = begin; b0 < end;) {
+        // the next pages' ids and scales
+        const int p0 = b0 >> shift;
+        const int np = min(kPageBlock, ((end - 1) >> shift) - p0 + 1);
+        const int bend = min(end, (p0 + np) << shift);
+        __syncthreads();
+        for (int i = threadIdx.x; i < np; i += kThreads) {
+            const int id = page_at(g, t.b, p0 + i);
+            const int64_t at = (int64_t)max(id, 0) * c.heads + h;
+            const float v = c.vs[at];
+            const float ve = v > 0.0f ? v : v == 0.0f ? 5.421010862e-20f : inf;  // zeros: any scale does; NaN as infinity
+            sm.id[i] = id;
+            sm.ks[i] = c.ks[at];
+            sm.lv[i] = log2f(ve);
+            sm.iv[i] = 1.0f / ve;
+        }
+        __syncthreads();
+
+        for (int t0 = b0 + warp * kStep; t0 < bend; t0 += kSplitTokens) {
+            const int p = (t0 >> shift) - p0, id = sm.id[p];
+            if (id < 0) continue;  // reported
+            const int64_t block = ((int64_t)id * c.heads + h) * c.page + (t0 & (c.page - 1));
+            const int8_t *kp = c.k + block * D + lg * D + 4 * kKWords * lt;
+            const int8_t *vp = c.v + block * D + 2 * lt * D + lg * (D / 8);
+            uint32_t kw[2][kSteps], vw[4][kVWords];
+#pragma unroll
+            for (int i = 0; i < kKChunks; ++i) {
+                load_words<kKWords>(kp + 16 * kKWords * i, &kw[0][kKWords * i]);
+                load_words<kKWords>(kp + 8 * D + 16 * kKWords * i, &kw[1][kKWords * i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) load_words<kVWords>(vp + ((i & 1) + 8 * (i >> 1)) * D, vw[i]);
+
+            float x[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const uint32_t a0 = codes_02(kw[0][s]), a1 = codes_02(kw[1][s]);
+                const uint32_t a2 = codes_02(kw[0][s] >> 8), a3 = codes_02(kw[1][s] >> 8);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma16816(x[n], a0, a1, a2, a3, qh[n][s][0], qh[n][s][1]);
+                    mma16816(x[n], a0, a1, a2, a3, ql[n][s][0], ql[n][s][1]);
+                }
+            }
+
+            // u = x + log2 vs for tokens t0 + lg (x[0], x[1]) and + 8 (x[2],
+            // x[3]) of rows 2 lt (x[0], x[2]) and 2 lt + 1
+            const float ks = sm.ks[p], lv = sm.lv[p], iv = sm.iv[p];
+            bool above = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = i & 1, j = t0 + lg + 8 * (i >> 1);
+                    const float u = fmaf(x[n][i], qf[n][r] * ks, lv);
+                    x[n][i] = j >= from[n][r] && j < to[n][r] ? u : -inf;
+                    above |= x[n][i] > m[n][r] + kRenew;
+                }
+            if (__any_sync(0xffffffffu, above)) {  // new references
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float v = fmaxf(x[n][r], x[n][r + 2]);
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        v = fmaxf(v - kTop, m[n][r]);
+                        const float f = m[n][r] == -inf ? 0.0f : ex2(m[n][r] - v);
+                        m[n][r] = v;
+                        l[n][r] *= f;
+#pragma unroll
+                        for (int s = 0; s < kSteps; ++s) {
+                            o[n][s][r] *= f;
+                            o[n][s][r + 2] *= f;
+                        }
+                    }
+            }
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float m0 = m[n][0] == -inf ? 0.0f : m[n][0], m1 = m[n][1] == -inf ? 0.0f : m[n][1];
+                const float w0 = ex2(x[n][0] - m0), w1 = ex2(x[n][1] - m1), w2 = ex2(x[n][2] - m0), w3 = ex2(x[n][3] - m1);
+                l[n][0] = fmaf(w0 + w2, iv, l[n][0]);
+                l[n][1] = fmaf(w1 + w3, iv, l[n][1]);
+                const uint32_t h0 = half_pair(w0, w1), h1 = half_pair(w2, w3);
+                ph[n][0] = transpose8(h0);
+                ph[n][1] = transpose8(h1);
+                pl[n][0] = transpose8(rest_pair(w0, w1, h0));
+                pl[n][1] = transpose8(rest_pair(w2, w3, h1));
+            }
+            // O^T: rows lg and lg + 8 of tile s are elements (D / 8) lg + 2 s and + 1
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const uint32_t sel = s & 1 ? 0x7632u : 0x5410u;
+                const uint32_t y = __byte_perm(vw[0][s / 2], vw[1][s / 2], sel), z = __byte_perm(vw[2][s / 2], vw[3][s / 2], sel);
+                const uint32_t a0 = codes_02(y), a1 = codes_02(y >> 8), a2 = codes_02(z), a3 = codes_02(z >> 8);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    // summed over the step by the tensor core, over the steps in
+                    // rounded fp32: its own sums are cut off, which a long
+                    // cache adds up (8192 tokens: 5e-6 against 1e-6)
+                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma16816(d, a0, a1, a2, a3, ph[n][0], ph[n][1]);
+                    mma16816(d, a0, a1, a2, a3, pl[n][0], pl[n][1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[n][s][i] += d[i];
+                }
+            }
+        }
+        b0 = bend;
+    }
+
+    // the warps' parts through shared memory, each relative to its own reference
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = 8 * n + 2 * lt + r;
+            float v = l[n][r];
+            v += __shfl_xor_sync(0xffffffffu, v, 4);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+            if (lg == 0) {
+                sm.ml[0][warp][row] = m[n][r];
+                sm.ml[1][warp][row] = v;
+            }
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                *reinterpret_cast<float2 *>(&sm.o[warp][row][(D / 8) * lg + 2 * s]) = make_float2(o[n][s][r], o[n][s][r + 2]);
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < t.rows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), d = 4 * (i - r * (D / 4));
+        float mm = sm.ml[0][0][r];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, sm.ml[0][w][r]);
+        float ll = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float mw = sm.ml[0][w][r], f = mw == -inf ? 0.0f : ex2(mw - mm);
+            // a warp without a reference holds zeros, or the NaN of a poisoned page
+            const float4 x = *reinterpret_cast<const float4 *>(&sm.o[w][r][d]);
+            const float lw = sm.ml[1][w][r];
+            ll = fmaf(f, lw, ll);
+            v.x = fmaf(f, x.x, v.x);
+            v.y = fmaf(f, x.y, v.y);
+            v.z = fmaf(f, x.z, v.z);
+            v.w = fmaf(f, x.w, v.w);
+        }
+        const int row = t.s.row0 + (t.r0 + r) / group, head = h * group + (t.r0 + r) % group;
+        const int64_t at = (int64_t)row * a.q_heads + head;
+        if (splits == 1) {
+            if (d == 0) write_lse(a, at, mm, ll);
+            write_out(a, at * D + d, v, ll);
+        } else {
+            float *to = part + ((((int64_t)blockIdx.x * c.heads + h) * gridDim.z + blockIdx.z) * kRows + r) * (D + 4);
+            if (d == 0) *reinterpret_cast<float2 *>(to) = make_float2(mm, ll);
+            *reinterpret_cast<float4 *>(to + 4 + d) = v;
+        }
+    }
+}
+
+// Joins the splits of a unit's rows; grid: (units, cached heads).
+__global__ void __launch_bounds__(kThreads)
+    kv_attention_join_kernel(const Cache c, const Batch g, const Attend a, int tile_rows, int chunk, int splits, const float *part) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int h = blockIdx.y, group = a.q_heads / c.heads, D = c.dim;
+    const Tile t = tile_of(g, a, c.page, group, tile_rows, blockIdx.x);
+    if (t.b < 0) return;
+    const int n = splits_of(t, chunk, splits);
+    if (n == 1) return;
+    const float inf = __int_as_float(0x7F800000);
+    const int64_t step = (int64_t)tile_rows * (D + 4);
+    for (int i = threadIdx.x; i < t.rows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), d = 4 * (i - r * (D / 4));
+        const float *p = part + (((int64_t)blockIdx.x * c.heads + h) * splits * tile_rows + r) * (D + 4);
+        float m = -inf;
+        for (int z = 0; z < n; ++z) m = fmaxf(m, p[z * step]);
+        float l = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int z = 0; z < n; ++z) {
+            const float2 ml = *reinterpret_cast<const float2 *>(p + z * step);
+            const float4 x = *reinterpret_cast<const float4 *>(p + z * step + 4 + d);
+            const float f = ml.x == -inf ? 0.0f : ex2(ml.x - m);
+            l = fmaf(f, ml.y, l);
+            v.x = fmaf(f, x.x, v.x);
+            v.y = fmaf(f, x.y, v.y);
+            v.z = fmaf(f, x.z, v.z);
+            v.w = fmaf(f, x.w, v.w);
+        }
+        const int row = t.s.row0 + (t.r0 + r) / group, head = h * group + (t.r0 + r) % group;
+        const int64_t at = (int64_t)row * a.q_heads + head;
+        if (d == 0) write_lse(a, at, m, l);
+        write_out(a, at * D + d, v, l);
+    }
+}
+
+// How a call is split: rows of a tile, upper bound of tiles, tokens and
+// number of splits.
+struct Plan {
+    int tile_rows;
+    int64_t units;
+    int chunk, splits;
+};
+Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv, int64_t window) {
+    Plan p;
+    const int64_t group = q_heads / heads;
+    // Sixteen rows where eight do not hold a sequence's: the cache is then
+    // read half as often. From 192 elements a head their registers do not fit.
+    p.tile_rows = dim <= 128 && group * (max_q > 1 ? max_q : 1) > 8 ? 16 : 8;
+    const int64_t seqs = T < batch ? T : batch;
+    p.units = T * group / p.tile_rows + seqs;
+    const int64_t tiles = (T * group + p.tile_rows - 1) / p.tile_rows;  // about as many have rows
+    int64_t kv = max_kv < 1 ? 1 : max_kv;
+    if (window && window + max_q < kv) kv = window + max_q;
+    // Enough CTAs for every SM to hold several, and for ragged lengths to even out.
+    const int64_t want = 8 * kSms / (tiles * heads > 0 ? tiles * heads : 1);
+    int64_t splits = want < 1 ? 1 : want;
+    const int64_t most = (kv + kSplitTokens - 1) / kSplitTokens;
+    if (splits > most) splits = most;
+    if (splits > 256) splits = 256;
+    p.chunk = (int)(((kv + splits - 1) / splits + kSplitTokens - 1) / kSplitTokens * kSplitTokens);
+    p.splits = (int)((kv + p.chunk - 1) / p.chunk);
+    return p;
+}
+
+template <int D, int NT>
+cudaError_t launch_tiles(const Cache &c, const Batch &g, const Rope &r, const Attend &a, const Plan &p, float *part, cudaStream_t s) {
+    static std::atomic<uint64_t> ready{0};  // devices whose shared memory limit is set
+    auto kernel = kv_attention_kernel<D, NT>;
+    constexpr int smem = (int)sizeof(Smem<D, NT>);
+    const cudaError_t es = allow_smem((const void *)kernel, smem, ready);
+    if (es != cudaSuccess) return es;
+    const dim3 grid((unsigned)p.units, (unsigned)c.heads, (unsigned)p.splits);
+    return launch(kernel, grid, kThreads, smem, s, c, g, r, a, p.chunk, part);
+}
+
+}  // namespace
+
+size_t kv_attention_bytes(int heads, int dim, int page, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv) {
+    (void)page;
+    // for any window: a window only lowers the number of splits' tokens, not their bound
+    const Plan p = plan_of(heads, dim, batch, q_heads, T, max_q, max_kv, 0);
+    return p.splits == 1 ? 0 : (size_t)p.units * heads * p.splits * p.tile_rows * (dim + 4) * 4;
+}
+
+cudaError_t launch_kv_attention(const Cache &c, const Batch &g, const Rope &r, const Attend &a, void *ws, cudaStream_t s) {
+    const Plan p = plan_of(c.heads, c.dim, g.batch, a.q_heads, g.T, a.max_q, a.max_kv, a.window);
+    float *part = static_cast<float *>(ws);
+    cudaError_t e;
+    const bool wide = p.tile_rows == 16;
+    switch (c.dim) {
+    case 64: e = wide ? launch_tiles<64, 2>(c, g, r, a, p, part, s) : launch_tiles<64, 1>(c, g, r, a, p, part, s); break;
+    case 96: e = wide ? launch_tiles<96, 2>(c, g, r, a, p, part, s) : launch_tiles<96, 1>(c, g, r, a, p, part, s); break;
+    case 128: e = wide ? launch_tiles<128, 2>(c, g, r, a, p, part, s) : launch_tiles<128, 1>(c, g, r, a, p, part, s); break;
+    case 192: e = launch_tiles<192, 1>(c, g, r, a, p, part, s); break;
+    default: e = launch_tiles<256, 1>(c, g, r, a, p, part, s); break;
+    }
+    if (e != cudaSuccess || p.splits == 1) return e;
+    return launch(kv_attention_join_kernel, dim3((unsigned)p.units, (unsigned)c.heads), kThreads, 0, s, c, g, a, p.tile_rows,
+                  p.chunk, p.splits, (const float *)part);
+}
+
+}  // namespace serving
+}  // namespace qmm

@@ -204,6 +204,7 @@ __host__ __device__ inline uint4 k4_header_to_canonical(const uint4 &h) {
 // ------------------------------------------------------------------ errors
 // Device error word bits (read and cleared by qmm_check_device_error).
 constexpr unsigned kDevErrTimeout = 1u;
+constexpr unsigned kDevErrRange = 2u;  // an offset, length or page id outside its array
 
 // A bounded wait gives up after this many SM clock cycles (about 2 s).
 constexpr long long kWaitTimeoutCycles = 4000000000LL;
@@ -482,6 +483,7 @@ unsigned *device_error_word();           // device pointer for the current devic
 cudaError_t ensure_smem_attr(const void *kernel, int bytes);
 int sm_count();                          // SMs of the current device
 void count_launch(unsigned n = 1);       // bump the launch counter
+void prepare_pool(cudaStream_t s);       // before cudaMallocAsync on the default memory pool
 qmm_status set_error(qmm_status s, const char *fmt, ...);
 
 // Kernel launchers (each .cu file); all return cudaSuccess or the launch error.

@@ -1,0 +1,244 @@
+// serving.cuh -- what the serving operators share: element types, the device
+// side of qmm_kv_cache / qmm_kv_batch / qmm_rope with its range checks, and
+// the launch helper.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "qmm_internal.cuh"
+
+namespace qmm {
+namespace serving {
+
+constexpr int kPageMax = 128, kHeadDimMax = 256;
+// SMs that work is split for. A constant, so that workspace sizes need no device.
+constexpr int kSms = 152;
+
+// ------------------------------------------------------------------ loads
+// Streamed reads of what earlier kernels wrote. Not the read-only path: a
+// kernel of this library may start while its predecessor still writes (and
+// waits for it), so its inputs are not constant over its lifetime.
+__device__ __forceinline__ uint4 ld128(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld64(const void *p) {
+    uint2 v;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ld32(const void *p) {
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+// ------------------------------------------------------------------ elements
+// Four consecutive elements as fp32 (p aligned to their size).
+template <int FT>
+__device__ __forceinline__ float4 load4(const void *p, int64_t i) {
+    if (FT == QMM_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+    if (FT == QMM_F16) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack_pair(int ft, float a, float b) {
+    if (ft == QMM_F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <int FT>
+__device__ __forceinline__ void store4(void *p, int64_t i, float4 v) {
+    if (FT == QMM_F32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = v;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) =
+            make_uint2(pack_pair(FT, v.x, v.y), pack_pair(FT, v.z, v.w));
+}
+__host__ __device__ inline int ftype_bytes(int ft) { return ft == QMM_F32 ? 4 : 2; }
+
+// ------------------------------------------------------------------ batch
+struct Batch {
+    const int32_t *table, *first, *length;
+    int batch, max_pages;
+    int64_t T, num_pages;
+    unsigned *err;
+};
+
+// Rows and cached tokens of sequence b: n rows from row0 on, len tokens with
+// them. Anything that does not fit the arrays (rows outside 0 .. T, more rows
+// than tokens, more tokens than the page table holds) is reported and reads
+// as a sequence without rows.
+struct Seq {
+    int row0, n, len;
+};
+__device__ __forceinline__ Seq seq_at(const Batch &g, int b, int page) {
+    Seq s;
+    s.row0 = g.first[b];
+    s.n = g.first[b + 1] - s.row0;
+    s.len = g.length[b];
+    const bool bad = s.row0 < 0 || s.n < 0 || (int64_t)s.row0 + s.n > g.T || s.len < s.n ||
+                     s.len > (int64_t)g.max_pages * page;
+    if (bad) {
+        atomicOr(g.err, kDevErrRange);
+        s.row0 = s.n = s.len = 0;
+    }
+    return s;
+}
+
+// Work units are numbered sequence by sequence, count(b) of them for sequence
+// b. The sequence that holds unit u and the unit's place in it, found by one
+// warp that scans the counts 32 at a time; b = -1 if there is no such unit.
+struct Unit {
+    int b, i;
+};
+template <class Count>
+__device__ __forceinline__ Unit find_unit(int64_t u, int batch, Count count) {
+    const int lane = threadIdx.x & 31;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < batch; b0 += 32) {
+        const int n = b0 + lane < batch ? count(b0 + lane) : 0;
+        int upto = n;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += o;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + upto > u);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            const int excl = __shfl_sync(0xffffffffu, upto - n, l);
+            return {b0 + l, (int)(u - before - excl)};
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return {-1, 0};
+}
+
+// Page id of page i of sequence b, -1 (reported) if it is not in the cache.
+__device__ __forceinline__ int page_at(const Batch &g, int b, int i) {
+    const int id = g.table[(int64_t)b * g.max_pages + i];
+    if (id >= 0 && id < g.num_pages) return id;
+    atomicOr(g.err, kDevErrRange);
+    return -1;
+}
+
+// ------------------------------------------------------------------ rotation
+struct Rope {
+    const float *table;
+    int dim, adjacent;  // dim 0: no rotation
+};
+
+// A head's elements are taken eight at a time, as two quads whose pairs turn
+// together: item j holds quads at quad_at(j).x and .y. For pairs (i, i +
+// dim / 2) the first dim / 8 items hold i = 4j .. 4j + 3 and their partners;
+// all other items are eight consecutive elements.
+__device__ __forceinline__ int2 quad_at(const Rope &r, int j) {
+    if (!r.adjacent && j < r.dim / 8) return make_int2(4 * j, 4 * j + r.dim / 2);
+    return make_int2(8 * j, 8 * j + 4);
+}
+// (a cos - b sin, a sin + b cos), each product and sum rounded by itself.
+__device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
+    const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+    b = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
+    a = x;
+}
+__device__ __forceinline__ void rotate_item(const Rope &r, int j, int64_t pos, float4 &a, float4 &b) {
+    if (j >= r.dim / 8) return;
+    const float4 *cs = reinterpret_cast<const float4 *>(r.table + (pos * (r.dim / 2) + 4 * j) * 2);
+    const float4 p = cs[0], q = cs[1];
+    if (r.adjacent) {
+        turn(a.x, a.y, p.x, p.y);
+        turn(a.z, a.w, p.z, p.w);
+        turn(b.x, b.y, q.x, q.y);
+        turn(b.z, b.w, q.z, q.w);
+    } else {
+        turn(a.x, b.x, p.x, p.y);
+        turn(a.y, b.y, p.z, p.w);
+        turn(a.z, b.z, q.x, q.y);
+        turn(a.w, b.w, q.z, q.w);
+    }
+}
+
+// ------------------------------------------------------------------ launch
+// Every serving kernel is launched so that it may start while its predecessor
+// ends, and waits for that one's results first (pdl_wait).
+template <class... P, class... A>
+inline cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+    count_launch();
+    return e;
+}
+
+// Lets `kernel` use `bytes` of shared memory on the current device, once per
+// device (`ready`: a bit each; devices past 64 set it every time).
+inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &ready) {
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = d < 64 ? (uint64_t)1 << d : 0;
+    if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+// ------------------------------------------------------------------ launchers
+struct Cache {
+    int8_t *k, *v;
+    float *ks, *vs;
+    int heads, page, dim;
+};
+struct Rows {  // the rows of one input: heads contiguous, `stride` elements from row to row
+    const void *p;
+    int64_t stride;
+};
+cudaError_t launch_kv_append(const Cache &c, const Batch &g, const Rope &r, int ft, Rows K, Rows V, cudaStream_t s);
+cudaError_t launch_kv_read(const Cache &c, const int32_t *pages, int64_t n, int64_t num_pages, int ft, void *K, void *V,
+                           unsigned *err, cudaStream_t s);
+
+struct Attend {
+    int ft, q_heads, causal;
+    float scale;  // of the scores, times log2 e
+    int64_t window, max_q, max_kv;
+    Rows Q;
+    void *out;
+    float *lse;
+};
+size_t kv_attention_bytes(int heads, int dim, int page, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv);
+cudaError_t launch_kv_attention(const Cache &c, const Batch &g, const Rope &r, const Attend &a, void *ws, cudaStream_t s);
+
+struct Logprobs {
+    int ft, G, top;
+    const void *X;
+    int64_t stride, M, V;
+    const int32_t *given;
+    float *lse, *entropy, *given_logp, *top_logp;
+    int32_t *top_ids;
+};
+size_t logprobs_bytes(int64_t M, int64_t V, int top);
+cudaError_t launch_logprobs(const Logprobs &a, void *ws, cudaStream_t s);
+
+}  // namespace serving
+}  // namespace qmm

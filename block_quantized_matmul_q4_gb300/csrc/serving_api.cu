@@ -1,0 +1,216 @@
+// serving_api.cu -- the extern "C" entry points of the serving operators
+// (include/qmm.h): argument checks, workspaces, dispatch to the launchers.
+#include "serving.cuh"
+
+namespace qmm {
+namespace serving {
+namespace {
+
+#define QMM_CHECK_ARG(cond, ...)                                 \
+    do {                                                         \
+        if (!(cond)) return set_error(QMM_ERR_ARG, __VA_ARGS__); \
+    } while (0)
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+qmm_status cuda_status(cudaError_t e, const char *what) {
+    if (e == cudaSuccess) {
+        set_error(QMM_OK, "%s", "");
+        return QMM_OK;
+    }
+    return set_error(QMM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+qmm_status nothing() { return cuda_status(cudaSuccess, ""); }
+
+qmm_status check_type(qmm_ftype t) {
+    QMM_CHECK_ARG(t == QMM_F32 || t == QMM_F16 || t == QMM_BF16, "element type must be F32, F16 or BF16 (got %d)", (int)t);
+    return QMM_OK;
+}
+
+qmm_status check_cache(const qmm_kv_cache *c) {
+    QMM_CHECK_ARG(c, "null cache");
+    QMM_CHECK_ARG(c->num_pages > 0 && c->num_pages <= INT32_MAX && c->heads > 0 && c->heads <= 65535,
+                  "cache needs 1 .. 2^31 - 1 pages and 1 .. 65535 heads (got %lld, %d)", (long long)c->num_pages, c->heads);
+    const int p = c->page_tokens, d = c->head_dim;
+    QMM_CHECK_ARG(p > 0 && d > 0, "page_tokens and head_dim must be positive (got %d, %d)", p, d);
+    if (p != 16 && p != 32 && p != 64 && p != 128)
+        return set_error(QMM_ERR_UNSUPPORTED, "page_tokens must be 16, 32, 64 or 128 (got %d)", p);
+    if (d != 64 && d != 96 && d != 128 && d != 192 && d != 256)
+        return set_error(QMM_ERR_UNSUPPORTED, "head_dim must be 64, 96, 128, 192 or 256 (got %d)", d);
+    QMM_CHECK_ARG(c->k && c->v && c->k_scale && c->v_scale, "null cache array");
+    QMM_CHECK_ARG(aligned(c->k, 16) && aligned(c->v, 16) && aligned(c->k_scale, 4) && aligned(c->v_scale, 4),
+                  "cache codes must be 16-byte aligned, scales 4-byte");
+    return QMM_OK;
+}
+
+qmm_status check_batch(const qmm_kv_batch *b, const qmm_kv_cache *c, int64_t T) {
+    QMM_CHECK_ARG(b, "null batch");
+    QMM_CHECK_ARG(T >= 0 && T <= INT32_MAX && b->batch >= 0, "need 0 <= T < 2^31 and batch >= 0 (T=%lld batch=%d)",
+                  (long long)T, b->batch);
+    if (T == 0 || b->batch == 0) return QMM_OK;
+    QMM_CHECK_ARG(b->table && b->first && b->length, "null batch array");
+    QMM_CHECK_ARG(aligned(b->table, 4) && aligned(b->first, 4) && aligned(b->length, 4), "batch arrays must be 4-byte aligned");
+    QMM_CHECK_ARG(b->max_pages > 0 && (int64_t)b->max_pages * c->page_tokens <= INT32_MAX,
+                  "max_pages must be positive and hold fewer than 2^31 tokens (got %d)", b->max_pages);
+    return QMM_OK;
+}
+
+qmm_status check_rope(const qmm_rope *r, const qmm_kv_cache *c, const qmm_kv_batch *b, Rope *out) {
+    *out = Rope{nullptr, 0, 0};
+    if (!r) return QMM_OK;
+    QMM_CHECK_ARG(r->table && aligned(r->table, 16), "rotation table must be non-null, 16-byte aligned");
+    QMM_CHECK_ARG(r->dim > 0 && r->dim % 8 == 0 && r->dim <= c->head_dim,
+                  "rotation dim must be a multiple of 8, at most head_dim (got %d)", r->dim);
+    QMM_CHECK_ARG(r->rows >= (int64_t)b->max_pages * c->page_tokens,
+                  "rotation table of %lld rows for %lld positions", (long long)r->rows,
+                  (long long)((int64_t)b->max_pages * c->page_tokens));
+    *out = Rope{r->table, r->dim, r->adjacent != 0};
+    return QMM_OK;
+}
+
+qmm_status check_rows(const void *p, int64_t stride, int64_t row, qmm_ftype t, const char *name) {
+    QMM_CHECK_ARG(p, "null pointer argument (%s)", name);
+    QMM_CHECK_ARG(stride >= row, "%s: rows of %lld elements are %lld apart", name, (long long)row, (long long)stride);
+    QMM_CHECK_ARG(aligned(p, 16) && stride % (16 / ftype_bytes(t)) == 0, "%s: rows must be 16-byte aligned", name);
+    return QMM_OK;
+}
+
+Batch batch_of(const qmm_kv_batch *b, const qmm_kv_cache *c, int64_t T) {
+    return Batch{b->table, b->first, b->length, b->batch, b->max_pages, T, c->num_pages, device_error_word()};
+}
+Cache cache_of(const qmm_kv_cache *c) {
+    return Cache{c->k, c->v, c->k_scale, c->v_scale, c->heads, c->page_tokens, c->head_dim};
+}
+
+// Runs `run` on the caller's workspace, or on one from the default memory
+// pool that lives until the work that `run` enqueues on `s` has finished.
+template <class F>
+qmm_status with_workspace(void *ws, size_t ws_bytes, size_t need, cudaStream_t s, F run) {
+    if (need == 0) return run(nullptr);
+    if (ws) {
+        QMM_CHECK_ARG(aligned(ws, 16), "workspace must be 16-byte aligned");
+        if (ws_bytes < need)
+            return set_error(QMM_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
+        return run(ws);
+    }
+    prepare_pool(s);
+    void *mem = nullptr;
+    const cudaError_t e = cudaMallocAsync(&mem, need, s);
+    if (e != cudaSuccess || !mem) {
+        cudaGetLastError();
+        return set_error(QMM_ERR_NOMEM, "cudaMallocAsync(%zu): %s", need, cudaGetErrorString(e));
+    }
+    const qmm_status st = run(mem);
+    const cudaError_t ef = cudaFreeAsync(mem, s);
+    if (st == QMM_OK && ef != cudaSuccess) return cuda_status(ef, "cudaFreeAsync");
+    return st;
+}
+
+}  // namespace
+}  // namespace serving
+}  // namespace qmm
+
+using namespace qmm;
+using namespace qmm::serving;
+
+#define QMM_TRY(expr)                       \
+    do {                                    \
+        const qmm_status st_ = (expr);      \
+        if (st_ != QMM_OK) return st_;      \
+    } while (0)
+
+extern "C" {
+
+qmm_status qmm_kv_append(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const qmm_rope *rope, qmm_ftype xt,
+                         const void *K, int64_t k_stride, const void *V, int64_t v_stride, int64_t T,
+                         qmm_stream_t stream) {
+    QMM_TRY(check_type(xt));
+    QMM_TRY(check_cache(cache));
+    QMM_TRY(check_batch(batch, cache, T));
+    if (T == 0 || batch->batch == 0) return nothing();
+    Rope r;
+    QMM_TRY(check_rope(rope, cache, batch, &r));
+    const int64_t row = (int64_t)cache->heads * cache->head_dim;
+    QMM_TRY(check_rows(K, k_stride, row, xt, "K"));
+    QMM_TRY(check_rows(V, v_stride, row, xt, "V"));
+    return cuda_status(launch_kv_append(cache_of(cache), batch_of(batch, cache, T), r, xt, Rows{K, k_stride},
+                                        Rows{V, v_stride}, (cudaStream_t)stream),
+                       "append launch");
+}
+
+qmm_status qmm_kv_read(const qmm_kv_cache *cache, const int32_t *pages, int64_t n, qmm_ftype xt, void *K, void *V,
+                       qmm_stream_t stream) {
+    QMM_TRY(check_type(xt));
+    QMM_TRY(check_cache(cache));
+    QMM_CHECK_ARG(n >= 0 && n <= INT32_MAX, "need 0 <= n < 2^31 pages (got %lld)", (long long)n);
+    if (n == 0) return nothing();
+    QMM_CHECK_ARG(pages && K && V, "null pointer argument");
+    QMM_CHECK_ARG(aligned(pages, 4) && aligned(K, 16) && aligned(V, 16), "K and V must be 16-byte aligned, pages 4-byte");
+    return cuda_status(launch_kv_read(cache_of(cache), pages, n, cache->num_pages, xt, K, V, device_error_word(),
+                                      (cudaStream_t)stream),
+                       "cache read launch");
+}
+
+size_t qmm_logprobs_workspace_bytes(int64_t M, int64_t V, int top) {
+    if (M <= 0 || V <= 0 || V > (1 << 20) || top < 0 || top > 32 || top > V) return 0;
+    return logprobs_bytes(M, V, top);
+}
+
+qmm_status qmm_logprobs(qmm_ftype xt, const void *X, int64_t x_stride, int64_t M, int64_t V, const int32_t *given, int G,
+                        int top, float *lse, float *entropy, float *given_logp, int32_t *top_ids, float *top_logp,
+                        void *workspace, size_t ws_bytes, qmm_stream_t stream) {
+    QMM_TRY(check_type(xt));
+    QMM_CHECK_ARG(M >= 0 && V >= 1 && top >= 0 && top <= V && G >= 0, "need M, G >= 0, V >= 1, 0 <= top <= V (M=%lld V=%lld top=%d G=%d)",
+                  (long long)M, (long long)V, top, G);
+    if (V > (1 << 20) || top > 32)
+        return set_error(QMM_ERR_UNSUPPORTED, "V=%lld (at most 2^20), top=%d (at most 32)", (long long)V, top);
+    QMM_CHECK_ARG(M <= (1 << 24), "M=%lld: at most 2^24 rows", (long long)M);
+    if (M == 0) return nothing();
+    QMM_CHECK_ARG(X && aligned(X, ftype_bytes(xt)), "X must be non-null and aligned to its elements");
+    QMM_CHECK_ARG(x_stride >= V, "rows of %lld elements are %lld apart", (long long)V, (long long)x_stride);
+    QMM_CHECK_ARG(!given_logp || G == 0 || given, "given_logp without given");
+    QMM_CHECK_ARG(top == 0 || (top_ids && top_logp), "top > 0 needs top_ids and top_logp");
+    QMM_CHECK_ARG(aligned(given, 4) && aligned(lse, 4) && aligned(entropy, 4) && aligned(given_logp, 4) && aligned(top_ids, 4) &&
+                      aligned(top_logp, 4), "outputs and given must be 4-byte aligned");
+    const Logprobs a = {xt, G, top, X, x_stride, M, V, given, lse, entropy, G ? given_logp : nullptr, top_logp, top_ids};
+    cudaStream_t s = (cudaStream_t)stream;
+    return with_workspace(workspace, ws_bytes, logprobs_bytes(M, V, top), s,
+                          [&](void *ws) { return cuda_status(launch_logprobs(a, ws, s), "logprobs launch"); });
+}
+
+size_t qmm_kv_attention_workspace_bytes(const qmm_kv_cache *cache, int batch, int q_heads, int64_t T, int64_t max_q,
+                                        int64_t max_kv) {
+    if (check_cache(cache) != QMM_OK || batch <= 0 || T <= 0 || T > INT32_MAX || q_heads <= 0 || q_heads % cache->heads) return 0;
+    return kv_attention_bytes(cache->heads, cache->head_dim, cache->page_tokens, batch, q_heads, T, max_q, max_kv);
+}
+
+qmm_status qmm_kv_attention(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const qmm_rope *rope, qmm_ftype qt,
+                            const void *Q, int64_t q_stride, int64_t T, int q_heads, float scale, int causal,
+                            int64_t window, int64_t max_q, int64_t max_kv, void *out, float *lse, void *workspace,
+                            size_t ws_bytes, qmm_stream_t stream) {
+    QMM_TRY(check_type(qt));
+    QMM_TRY(check_cache(cache));
+    QMM_TRY(check_batch(batch, cache, T));
+    QMM_CHECK_ARG(q_heads > 0 && q_heads % cache->heads == 0, "q_heads=%d is not a multiple of the cache's %d heads", q_heads,
+                  cache->heads);
+    QMM_CHECK_ARG(q_heads / cache->heads <= 256, "at most 256 query heads for a cached one (got %d)", q_heads / cache->heads);
+    QMM_CHECK_ARG(T * (q_heads / cache->heads) <= INT32_MAX, "T=%lld rows of %d heads are too many", (long long)T, q_heads);
+    QMM_CHECK_ARG(window >= 0 && (window == 0 || causal), "window must be >= 0, and 0 without causal (got %lld)", (long long)window);
+    QMM_CHECK_ARG(max_q >= 0 && max_kv >= 0, "max_q and max_kv must be >= 0");
+    QMM_CHECK_ARG(scale > 0.0f && scale < 3.0e38f, "scale must be positive and finite");
+    if (T == 0 || batch->batch == 0) return nothing();
+    Rope r;
+    QMM_TRY(check_rope(rope, cache, batch, &r));
+    QMM_TRY(check_rows(Q, q_stride, (int64_t)q_heads * cache->head_dim, qt, "Q"));
+    QMM_CHECK_ARG(out && aligned(out, 16) && aligned(lse, 4), "out must be non-null and 16-byte aligned, lse 4-byte");
+    constexpr float kLog2e = 1.44269504088896f;
+    const Attend a = {qt, q_heads, causal != 0, scale * kLog2e, window, max_q, max_kv, Rows{Q, q_stride}, out, lse};
+    cudaStream_t s = (cudaStream_t)stream;
+    const size_t need = kv_attention_bytes(cache->heads, cache->head_dim, cache->page_tokens, batch->batch, q_heads, T, max_q,
+                                           max_kv);
+    return with_workspace(workspace, ws_bytes, need, s, [&](void *ws) {
+        return cuda_status(launch_kv_attention(cache_of(cache), batch_of(batch, cache, T), r, a, ws, s), "attention launch");
+    });
+}
+
+}  // extern "C"

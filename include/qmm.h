@@ -42,7 +42,8 @@
  *   - Errors: arguments are validated before anything is enqueued; on any
  *     error nothing is launched and a qmm_status other than QMM_OK is
  *     returned (qmm_last_error() gives a one-line reason). Kernels never trap:
- *     a device-side wait that exceeds its bound records QMM_ERR_TIMEOUT in a
+ *     a device-side wait that exceeds its bound records QMM_ERR_TIMEOUT, an
+ *     offset in device memory that points outside its array QMM_ERR_ARG, in a
  *     device error word, read and cleared by qmm_check_device_error.
  */
 #ifndef QMM_H
@@ -406,6 +407,143 @@ qmm_status qmm_w4a16_lut(const void *W_packed, const uint16_t *scales, const uin
 qmm_status qmm_w4a16_unpack_zeros(const uint32_t *zeros_packed, uint8_t *zeros, int64_t N,
                                   int64_t ngroups, qmm_stream_t stream);
 
+/* ---------------------------------------------------------------- serving
+ * The operators between a decoder layer's products: keys and values into a
+ * paged 8-bit cache, attention over that cache, and token log probabilities
+ * of the head's product. Their inputs and outputs are fp32 (what qmm_mul_mat
+ * reads and writes), fp16 (what qmm_w4a16 does) or bf16. They follow the
+ * conventions above (device pointers, streams, errors), and they launch with
+ * programmatic dependent launch: they read nothing before the preceding
+ * kernel on the stream has completed.
+ *
+ * What the host cannot check -- row offsets, lengths and page ids live in
+ * device memory -- the kernels check before they use it: a sequence or page
+ * that points outside its arrays is left out (its results are unspecified),
+ * and the next qmm_check_device_error on the device returns QMM_ERR_ARG. */
+typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_ftype;
+
+/* A layer's cache of keys and values in 8 bits: pages of page_tokens tokens,
+ * [num_pages][heads][page_tokens][head_dim] int8 codes, and one fp32 scale
+ * for each page and head: value = code * scale. heads are the cached heads
+ * (the query heads of qmm_kv_attention are a multiple of them). page_tokens:
+ * 16, 32, 64 or 128; head_dim: 64, 96, 128, 192 or 256 (QMM_ERR_UNSUPPORTED
+ * otherwise). k and v 16-byte aligned, the scales 4-byte. The memory needs
+ * no initial values: a page is overwritten from its first slot on. */
+typedef struct {
+    int8_t *k, *v;
+    float *k_scale, *v_scale; /* [num_pages][heads] */
+    int64_t num_pages;
+    int heads, page_tokens, head_dim;
+} qmm_kv_cache;
+
+/* The sequences of one call. Rows first[b] .. first[b + 1] - 1 of its inputs
+ * are the newest tokens of sequence b, which has length[b] tokens in the
+ * cache once they are in: row first[b] + i is the token at position
+ * length[b] - (first[b + 1] - first[b]) + i. Token j of the sequence is in
+ * slot j % page_tokens of page table[b * max_pages + j / page_tokens];
+ * entries that no token needs are not read. The three arrays are device
+ * memory, first has batch + 1 entries. A sequence may have no rows. */
+typedef struct {
+    const int32_t *table, *first, *length;
+    int batch, max_pages;
+} qmm_kv_batch;
+
+/* Position rotation: each of the dim / 2 pairs (a, b) of a head's first dim
+ * elements becomes (a cos - b sin, a sin + b cos) with (cos, sin) =
+ * table[position][pair], fp32 [rows][dim / 2][2], rows at least max_pages *
+ * page_tokens, 16-byte aligned. Pair i is the elements (i, i + dim / 2), or
+ * (2i, 2i + 1) where adjacent is not 0. dim is a multiple of 8 (at most
+ * head_dim); elements from dim on stay. A table rather than a base frequency, so that
+ * any rescaling of positions or frequencies is the caller's. */
+typedef struct {
+    const float *table;
+    int64_t rows;
+    int dim, adjacent;
+} qmm_rope;
+
+/* Append the rows of K and V ([T][heads][head_dim], type xt; a row's heads
+ * are contiguous, rows k_stride / v_stride elements apart, so both may be
+ * slices of one product) to the cache, K rotated by `rope` on the way (NULL:
+ * as it is). All T = first[batch] rows are quantized per page and head:
+ *   a = max |x| over the new slots, d = a / 127, at least the scale of the
+ *   page if slots before the first new one keep their tokens;
+ *   the block's other codes: if d grew, round(code * (old / d));  new ones:
+ *   round(x * (1 / d)), both half away from zero, in IEEE fp32.
+ * A page whose slot 0 is among the new ones keeps nothing (its old scale
+ * does not count), so recycled pages need no clearing. d below 2^-126 counts
+ * as 0 (codes 0). If a new value is an infinity or a NaN, d is infinite and
+ * the block's codes are 0: everything read from that page and head is NaN.
+ * Two sequences of one call must not append to the same page.
+ * K, V: 16-byte aligned rows (strides a multiple of 16 bytes).
+ * Errors: QMM_ERR_ARG, QMM_ERR_UNSUPPORTED (sizes), QMM_ERR_CUDA. T == 0 or
+ * batch == 0 is a no-op. */
+qmm_status qmm_kv_append(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const qmm_rope *rope,
+                         qmm_ftype xt, const void *K, int64_t k_stride, const void *V,
+                         int64_t v_stride, int64_t T, qmm_stream_t stream);
+
+/* The values that n pages of the cache hold: K and V [n][heads][page_tokens]
+ * [head_dim] of type xt (16-byte aligned, contiguous), code * scale in fp32
+ * rounded once. pages: device array of n page ids. Slots that no token was
+ * appended to give whatever their codes say. For moving, saving or checking
+ * a cache. n == 0 is a no-op. */
+qmm_status qmm_kv_read(const qmm_kv_cache *cache, const int32_t *pages, int64_t n, qmm_ftype xt,
+                       void *K, void *V, qmm_stream_t stream);
+
+/* Attention of the batch's rows over the cache (which already holds their own
+ * tokens). Q [T][q_heads][head_dim] of type qt, rows q_stride elements apart
+ * (16-byte aligned), is rotated by `rope` on the way (NULL: as it is); query
+ * head h reads cached head h / (q_heads / heads). A row at position p sees
+ * the tokens j <= p, with window > 0 only those j > p - window, with causal
+ * == 0 every token of its sequence:
+ *   x_j = scale * (q . k_j),  lse = log sum_j e^x_j,  out = sum_j e^(x_j - lse) v_j
+ * out: [T][q_heads][head_dim] contiguous, type qt, 16-byte aligned; lse: fp32
+ * [T][q_heads] or NULL. A row that sees nothing gives out = 0, lse = -inf.
+ * Arithmetic: the codes are exact in fp16; q is taken as a sum of two fp16
+ * numbers times a power of two per row and head (22 bits), the
+ * probabilities as two fp16 numbers where qt is fp32 or the call is a decode
+ * step (one where not); tensor cores with fp32 accumulation; page scales,
+ * maxima and sums in fp32.
+ * max_q, max_kv: the largest number of rows and the largest length of any
+ * sequence as the caller knows them. They choose kernels and how the work is
+ * split; results do not depend on them being right.
+ * workspace: qmm_kv_attention_workspace_bytes(...) bytes, 16-byte aligned, in
+ * use until the call's work on `stream` has finished; NULL: the call takes
+ * it from the device's default memory pool, stream-ordered.
+ * Errors: QMM_ERR_ARG, QMM_ERR_UNSUPPORTED, QMM_ERR_WORKSPACE, QMM_ERR_NOMEM,
+ * QMM_ERR_CUDA. T == 0 or batch == 0 is a no-op. */
+size_t qmm_kv_attention_workspace_bytes(const qmm_kv_cache *cache, int batch, int q_heads, int64_t T,
+                                        int64_t max_q, int64_t max_kv);
+qmm_status qmm_kv_attention(const qmm_kv_cache *cache, const qmm_kv_batch *batch, const qmm_rope *rope,
+                            qmm_ftype qt, const void *Q, int64_t q_stride, int64_t T, int q_heads,
+                            float scale, int causal, int64_t window, int64_t max_q, int64_t max_kv,
+                            void *out, float *lse, void *workspace, size_t ws_bytes,
+                            qmm_stream_t stream);
+
+/* Log probabilities from logits X [M][V] of type xt, rows x_stride elements
+ * apart (X aligned to its type). Each output may be NULL (not wanted):
+ *   lse [M]             log sum_v e^X[m, v]
+ *   entropy [M]         -sum_v p_v log p_v, in nats
+ *   given_logp [M][G]   X[m, given[m, g]] - lse (taken as (X - max) - (lse -
+ *                       max)), given int32 [M][G]; an id outside 0 .. V - 1
+ *                       gives NaN
+ *   top_ids, top_logp [M][top]  the `top` most likely tokens in falling
+ *                       order, equal logits by rising id, and their log
+ *                       probabilities (both or neither)
+ * all fp32 but the int32 ids. 1 <= V <= 2^20, 0 <= top <= min(V, 32)
+ * (QMM_ERR_UNSUPPORTED above 2^20 or 32). Logits of -inf have probability 0;
+ * a row with nothing else gives lse = -inf, entropy 0 and log probabilities
+ * of -inf. A NaN or +inf in a row makes its lse, entropy and log
+ * probabilities NaN; its ids rank NaN above +inf.
+ * workspace: qmm_logprobs_workspace_bytes(M, V, top) bytes (may be 0), 16-byte
+ * aligned; NULL: taken from the default memory pool, stream-ordered.
+ * Errors: QMM_ERR_ARG, QMM_ERR_UNSUPPORTED, QMM_ERR_WORKSPACE, QMM_ERR_NOMEM,
+ * QMM_ERR_CUDA. M == 0 is a no-op. */
+size_t qmm_logprobs_workspace_bytes(int64_t M, int64_t V, int top);
+qmm_status qmm_logprobs(qmm_ftype xt, const void *X, int64_t x_stride, int64_t M, int64_t V,
+                        const int32_t *given, int G, int top, float *lse, float *entropy,
+                        float *given_logp, int32_t *top_ids, float *top_logp, void *workspace,
+                        size_t ws_bytes, qmm_stream_t stream);
+
 /* Per-block integer sums of the factored form, for bit-exact checking
  * (page 1, "正确性" and "通用实现"). Xq holds canonical activation blocks
  * (Q8_0 for Q4_0 weights, Q8_K for Q4_K and Q6_K), M rows.
@@ -465,8 +603,9 @@ const char *qmm_last_error(void);
 
 /* Synchronize `stream`, then read and clear the device error word of the
  * current device. Returns QMM_ERR_TIMEOUT if a kernel gave up a bounded
- * wait since the last check, QMM_ERR_CUDA if the stream reported an error,
- * QMM_OK otherwise. */
+ * wait since the last check, QMM_ERR_ARG if a serving operator met a row
+ * offset, length or page id outside its arrays, QMM_ERR_CUDA if the stream
+ * reported an error, QMM_OK otherwise. */
 qmm_status qmm_check_device_error(qmm_stream_t stream);
 
 /* Number of kernels this library has launched on this process (all devices).
