@@ -17,6 +17,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kLog2e = 1.44269504088896f;
 constexpr int kTopMax = 32;
+constexpr int kFoundMax = 256;  // one for each thread: candidates rank themselves
+static_assert(kFoundMax <= kThreads, "a thread for each candidate");
 constexpr int64_t kVocabMax = (int64_t)1 << 20;
 // Elements of a chunk for each thread: 64, or 16 where that leaves SMs idle
 // (see chunk_elems).
@@ -46,6 +48,19 @@ __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
     const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
     return (uint64_t)hi << 32 | lo;
+}
+
+// The warp's values in falling order, the largest in lane 0 (bitonic).
+__device__ __forceinline__ float warp_sort_falling(float v, int lane) {
+#pragma unroll
+    for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
+        for (int j = k / 2; j; j /= 2) {
+            const float o = __shfl_xor_sync(0xffffffffu, v, j);
+            // the lower lane of a falling run keeps the larger value
+            v = ((lane & j) == 0) == ((lane & k) == 0) ? fmaxf(v, o) : fminf(v, o);
+        }
+    return v;
 }
 
 struct Stats {
@@ -89,10 +104,137 @@ __device__ __forceinline__ void finish_row(const Logprobs &a, int64_t row, Stats
     }
 }
 
+// Pairs of fp32 values: one instruction for two.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// A chunk of a row: `vecs` 16-byte vectors for each thread, vector i of thread
+// j at elements first + (i * kThreads + j) * (16 / element size) and on, those
+// of them that are in 0 .. V - 1.
+struct Chunk {
+    const char *row;
+    int64_t first, V;
+    int vecs;
+};
+
+// The chunk's `n` largest keys in falling order by rounds of a CTA-wide
+// maximum, read from memory each time: for chunks with many equal logits or a
+// NaN, which largest_keys does not take.
+template <int FT>
+__device__ __noinline__ void largest_keys_by_rounds(const Chunk c, int n, uint64_t *top, uint64_t (*best_of)[kThreads / 32]) {
+    constexpr int kVec = FT == QMM_F32 ? 4 : 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t mine = 0, last = ~0ull;
+    for (int k = 0; k < n; ++k) {
+        if (k == 0 || mine == last) {  // this thread's largest key below the last one taken
+            mine = 0;
+            for (int i = 0; i < c.vecs; ++i)
+                for (int j = 0; j < kVec; ++j) {
+                    const int64_t e = c.first + ((int64_t)i * kThreads + threadIdx.x) * kVec + j;
+                    const uint64_t key = e >= 0 && e < c.V ? key_of(load_one<FT>(c.row, e), (uint32_t)e) : 0;
+                    if (key < last && key > mine) mine = key;
+                }
+        }
+        const uint64_t w = warp_max_key(mine);
+        if (lane == 0) best_of[k & 1][warp] = w;
+        __syncthreads();
+        last = 0;
+        for (int i = 0; i < kThreads / 32; ++i) last = best_of[k & 1][i] > last ? best_of[k & 1][i] : last;
+        if (threadIdx.x == 0) top[k] = last;
+    }
+    __syncthreads();
+}
+
+// The chunk's `n` largest keys in falling order; most: this thread's largest
+// element. The n-th largest of the threads' maxima, tau, bounds the n-th
+// largest element from below, so the elements >= tau (little more than n of
+// them) hold the answer. Each warp sorts its maxima, every thread ranks its
+// one among all by binary searches, the warps read the elements of the
+// threads that reach tau once more, and the elements found rank themselves by
+// counting. False where more are found than fit.
+template <int FT>
+__device__ __forceinline__ bool largest_keys(const Chunk c, int n, float most, uint64_t *top) {
+    constexpr int kVec = FT == QMM_F32 ? 4 : 8;
+    __shared__ float maxima[kThreads / 32][32];
+    __shared__ float tau_at;
+    __shared__ int threads, count;
+    __shared__ int16_t reach[kThreads];
+    __shared__ uint64_t found[kFoundMax];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float sorted = warp_sort_falling(most, lane);
+    maxima[warp][lane] = sorted;
+    if (threadIdx.x == 0) threads = count = 0;
+    if ((int)threadIdx.x < n) top[threadIdx.x] = 0;
+    __syncthreads();
+    int rank = lane;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        // warp w's maxima that come before this one (equal ones: by warp)
+        int before = 0;
+#pragma unroll
+        for (int step = 16; step; step /= 2) {
+            const float v = maxima[w][before + step - 1];
+            before += v > sorted || (v == sorted && w < warp) ? step : 0;
+        }
+        const float v = maxima[w][before];
+        before += v > sorted || (v == sorted && w < warp) ? 1 : 0;
+        rank += w == warp ? 0 : before;
+    }
+    if (rank == n - 1) tau_at = sorted;
+    __syncthreads();
+    const float tau = tau_at;
+    if (most >= tau) reach[atomicAdd(&threads, 1)] = (int16_t)threadIdx.x;
+    __syncthreads();
+    for (int t = warp; t < threads; t += kThreads / 32)
+        for (int i = lane; i < c.vecs * kVec; i += 32) {
+            const int64_t e = c.first + ((int64_t)(i / kVec) * kThreads + reach[t]) * kVec + i % kVec;
+            if (e < 0 || e >= c.V) continue;
+            const float x = load_one<FT>(c.row, e);
+            if (x >= tau) {
+                const int at = atomicAdd(&count, 1);
+                if (at < kFoundMax) found[at] = key_of(x, (uint32_t)e);
+            }
+        }
+    __syncthreads();
+    const int all = count;
+    if (all > kFoundMax) return false;
+    if ((int)threadIdx.x < all) {
+        const uint64_t key = found[threadIdx.x];
+        int before = 0;
+        for (int i = 0; i < all; ++i) before += found[i] > key;
+        if (before < n) top[before] = key;
+    }
+    __syncthreads();
+    return true;
+}
+
 // grid: rows x chunks. stats [row][chunk] and keys [row][chunk][top] where a
 // row has several chunks.
 template <int FT, int ELTS>
-__global__ void __launch_bounds__(kThreads) logprobs_chunk_kernel(const Logprobs a, int chunks, Stats *stats, uint64_t *keys) {
+__global__ void __launch_bounds__(kThreads, 3) logprobs_chunk_kernel(const Logprobs a, int chunks, Stats *stats, uint64_t *keys) {
     constexpr int kVec = FT == QMM_F32 ? 4 : 8;
     constexpr int kVecs = ELTS / kVec;
     __shared__ float red[3][kThreads / 32];
@@ -107,18 +249,20 @@ __global__ void __launch_bounds__(kThreads) logprobs_chunk_kernel(const Logprobs
 
     // the chunk as 16-byte vectors of the row's aligned addresses; vectors
     // that the row's ends cut are read element by element
-    const int esize = ftype_bytes(FT);
-    const char *p = static_cast<const char *>(a.X) + row * a.stride * esize;
-    const int skew = (int)((uintptr_t)p % 16) / esize;
+    constexpr int kSize = FT == QMM_F32 ? 4 : 2;
+    Chunk c;
+    c.row = static_cast<const char *>(a.X) + row * a.stride * kSize;
+    c.V = a.V;
+    c.first = (int64_t)chunk * kVecs * kThreads * kVec - (int)((uintptr_t)c.row % 16) / kSize;
+    const int64_t left = (a.V - c.first + kThreads * kVec - 1) / (kThreads * kVec);
+    c.vecs = left < kVecs ? (int)left : kVecs;  // the last chunk may hold few
     float x[ELTS];
-    float most = -inf;
-    const int64_t e0 = ((int64_t)chunk * kVecs * kThreads + threadIdx.x) * kVec - skew;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-        const int64_t e = e0 + (int64_t)i * kThreads * kVec;
+        const int64_t e = c.first + ((int64_t)i * kThreads + threadIdx.x) * kVec;
         float *v = x + i * kVec;
-        if (e >= 0 && e + kVec <= a.V) {
-            const uint4 u = ld128(p + e * esize);
+        if (i < c.vecs && e >= 0 && e + kVec <= a.V) {
+            const uint4 u = ld128(c.row + e * kSize);
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -135,14 +279,16 @@ __global__ void __launch_bounds__(kThreads) logprobs_chunk_kernel(const Logprobs
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] = e + k >= 0 && e + k < a.V ? load_one<FT>(p, e + k) : -inf;
+            for (int k = 0; k < kVec; ++k) v[k] = e + k >= 0 && e + k < a.V ? load_one<FT>(c.row, e + k) : -inf;
         }
     }
+    float mine = -inf;
 #pragma unroll
-    for (int i = 0; i < ELTS; ++i) most = fmaxf(most, x[i]);
+    for (int i = 0; i < ELTS; ++i) mine = fmaxf(mine, x[i]);
 
     // the chunk's sums
     Stats s;
+    float most = mine;
 #pragma unroll
     for (int d = 16; d; d /= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
     if (lane == 0) red[0][warp] = most;
@@ -150,14 +296,21 @@ __global__ void __launch_bounds__(kThreads) logprobs_chunk_kernel(const Logprobs
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) most = fmaxf(most, red[0][w]);
     s.m = most == -inf ? 0.0f : most;
-    s.l = s.t = 0.0f;
+    uint64_t l2 = pair(0.0f, 0.0f), t2 = l2;
+    const uint64_t minus = pair(-s.m, -s.m), log2e = pair(kLog2e, kLog2e);
 #pragma unroll
-    for (int i = 0; i < ELTS; ++i) {
-        const float d = (x[i] - s.m) * kLog2e;
-        const float e = ex2(d);
-        s.l += e;
-        s.t = fmaf(e, fmaxf(d, -1000.0f), s.t);  // 0, not 0 * -inf, where x = -inf
-    }
+    for (int i = 0; i < kVecs; ++i)
+        if (i < c.vecs)
+#pragma unroll
+            for (int k = 0; k < kVec; k += 2) {
+                const uint64_t d = mul2(add2(pair(x[i * kVec + k], x[i * kVec + k + 1]), minus), log2e);
+                const float2 f = unpair(d);
+                const uint64_t e = pair(ex2(f.x), ex2(f.y));
+                l2 = add2(l2, e);
+                t2 = fma2(e, pair(fmaxf(f.x, -1000.0f), fmaxf(f.y, -1000.0f)), t2);  // 0, not 0 * -inf, where x = -inf
+            }
+    s.l = unpair(l2).x + unpair(l2).y;
+    s.t = unpair(t2).x + unpair(t2).y;
 #pragma unroll
     for (int d = 16; d; d /= 2) {
         s.l += __shfl_xor_sync(0xffffffffu, s.l, d);
@@ -175,30 +328,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_chunk_kernel(const Logprobs
         s.t += red[2][w];
     }
 
-    // the chunk's largest keys: rounds of a CTA-wide maximum; the thread that
-    // held it looks for its next one
-    if (a.top) {
-        uint64_t mine = 0, last = ~0ull;
-        for (int k = 0; k < a.top; ++k) {
-            if (k == 0 || mine == last) {
-                mine = 0;
-#pragma unroll
-                for (int i = 0; i < ELTS; ++i) {
-                    const int64_t e = e0 + (int64_t)(i / kVec) * kThreads * kVec + i % kVec;
-                    const uint64_t key = e >= 0 && e < a.V ? key_of(x[i], (uint32_t)e) : 0;
-                    if (key < last && key > mine) mine = key;
-                }
-            }
-            const uint64_t w = warp_max_key(mine);
-            if (lane == 0) best_of[k & 1][warp] = w;
-            __syncthreads();
-            last = 0;
-#pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i) last = best_of[k & 1][i] > last ? best_of[k & 1][i] : last;
-            if (threadIdx.x == 0) top[k] = last;
-        }
-        __syncthreads();
-    }
+    // a NaN, which the maxima pass over, shows in the sum
+    if (a.top && (s.l != s.l || !largest_keys<FT>(c, a.top, mine, top))) largest_keys_by_rounds<FT>(c, a.top, top, best_of);
     if (chunks == 1) {
         finish_row<FT>(a, row, s, top);
         return;
