@@ -5,9 +5,9 @@
 // give  lse = m + ln 2 log2 l  and  entropy = (log2 l - t / l) ln 2;  sums with
 // references m_c join with d_c = (m_c - m) log2 e as  l = sum 2^d_c l_c,  t =
 // sum 2^d_c (t_c + d_c l_c). (The difference is taken before the product:
-// logits masked with the type's lowest value would overflow it.)  A CTA holds a chunk of a row in
-// registers, so the maximum comes before the exponentials without a second
-// read; a row of several chunks is joined by a second kernel.
+// logits masked with the type's lowest value would overflow it.) A CTA takes a
+// chunk of a row, its maximum first; a row of several chunks is joined by a
+// second kernel. What bounds it: reading the logits once.
 #include "serving.cuh"
 
 namespace qmm {
@@ -20,11 +20,8 @@ constexpr int kTopMax = 32;
 constexpr int kFoundMax = 256;  // one for each thread: candidates rank themselves
 static_assert(kFoundMax <= kThreads, "a thread for each candidate");
 constexpr int64_t kVocabMax = (int64_t)1 << 20;
-// Elements of a chunk for each thread: 64, or 16 where that leaves SMs idle
-// (see chunk_elems).
-constexpr int kEltsLarge = 64, kEltsSmall = 16;
-constexpr int kListsMax = 96;  // chunks of a row: kVocabMax / (256 * 64) and one more, or kSmallChunksMax
-constexpr int kSmallChunksMax = 64;
+constexpr int kChunkLarge = 32768, kChunkSmall = 8192;  // bytes (see chunks_of)
+constexpr int kListsMax = 160, kSmallChunksMax = 128;    // chunks of a row
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -48,19 +45,6 @@ __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
     const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
     return (uint64_t)hi << 32 | lo;
-}
-
-// The warp's values in falling order, the largest in lane 0 (bitonic).
-__device__ __forceinline__ float warp_sort_falling(float v, int lane) {
-#pragma unroll
-    for (int k = 2; k <= 32; k *= 2)
-#pragma unroll
-        for (int j = k / 2; j; j /= 2) {
-            const float o = __shfl_xor_sync(0xffffffffu, v, j);
-            // the lower lane of a falling run keeps the larger value
-            v = ((lane & j) == 0) == ((lane & k) == 0) ? fmaxf(v, o) : fminf(v, o);
-        }
-    return v;
 }
 
 struct Stats {
@@ -104,6 +88,11 @@ __device__ __forceinline__ void finish_row(const Logprobs &a, int64_t row, Stats
     }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 // Pairs of fp32 values: one instruction for two.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
     uint64_t r;
@@ -131,18 +120,17 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
-// A chunk of a row: `vecs` 16-byte vectors for each thread, vector i of thread
-// j at elements first + (i * kThreads + j) * (16 / element size) and on, those
-// of them that are in 0 .. V - 1.
+// A chunk of a row: `n` 16-byte vectors from element `first` on, vector v held
+// by thread v % kThreads; of their elements those in 0 .. V - 1 count.
 struct Chunk {
     const char *row;
     int64_t first, V;
-    int vecs;
+    int n;
 };
 
 // The chunk's `n` largest keys in falling order by rounds of a CTA-wide
-// maximum, read from memory each time: for chunks with many equal logits or a
-// NaN, which largest_keys does not take.
+// maximum, read from memory each time: for chunks with a NaN, and for what
+// largest_keys does not take.
 template <int FT>
 __device__ __noinline__ void largest_keys_by_rounds(const Chunk c, int n, uint64_t *top, uint64_t (*best_of)[kThreads / 32]) {
     constexpr int kVec = FT == QMM_F32 ? 4 : 8;
@@ -151,9 +139,9 @@ __device__ __noinline__ void largest_keys_by_rounds(const Chunk c, int n, uint64
     for (int k = 0; k < n; ++k) {
         if (k == 0 || mine == last) {  // this thread's largest key below the last one taken
             mine = 0;
-            for (int i = 0; i < c.vecs; ++i)
+            for (int v = threadIdx.x; v < c.n; v += kThreads)
                 for (int j = 0; j < kVec; ++j) {
-                    const int64_t e = c.first + ((int64_t)i * kThreads + threadIdx.x) * kVec + j;
+                    const int64_t e = c.first + (int64_t)v * kVec + j;
                     const uint64_t key = e >= 0 && e < c.V ? key_of(load_one<FT>(c.row, e), (uint32_t)e) : 0;
                     if (key < last && key > mine) mine = key;
                 }
@@ -168,78 +156,130 @@ __device__ __noinline__ void largest_keys_by_rounds(const Chunk c, int n, uint64
     __syncthreads();
 }
 
-// The chunk's `n` largest keys in falling order; most: this thread's largest
-// element. The n-th largest of the threads' maxima, tau, bounds the n-th
-// largest element from below, so the elements >= tau (little more than n of
-// them) hold the answer. Each warp sorts its maxima, every thread ranks its
-// one among all by binary searches, the warps read the elements of the
-// threads that reach tau once more, and the elements found rank themselves by
-// counting. False where more are found than fit.
+// This warp's p-th largest thread maximum (p >= 1): the largest is left out,
+// from one thread, p - 1 times.
+__device__ __forceinline__ float warp_nth_largest(float mine, int p) {
+    const int lane = threadIdx.x & 31;
+    uint32_t order = (uint32_t)(key_of(mine, 0) >> 32);
+    for (; p > 1; --p) {
+        const uint32_t largest = __reduce_max_sync(0xffffffffu, order);
+        if (lane == __ffs(__ballot_sync(0xffffffffu, order == largest)) - 1) order = 0;
+    }
+    return key_value((uint64_t)__reduce_max_sync(0xffffffffu, order) << 32);
+}
+
+// The first `n` keys of a chunk with many elements equal to tau, into
+// found[0 .. n - 1] in any order: those above tau, and the first of the equal
+// ones by index. False where those above it are more than kFoundMax.
 template <int FT>
-__device__ __forceinline__ bool largest_keys(const Chunk c, int n, float most, uint64_t *top) {
-    constexpr int kVec = FT == QMM_F32 ? 4 : 8;
-    __shared__ float maxima[kThreads / 32][32];
-    __shared__ float tau_at;
-    __shared__ int threads, count;
-    __shared__ int16_t reach[kThreads];
-    __shared__ uint64_t found[kFoundMax];
+__device__ __noinline__ bool keys_above_and_equal(const Chunk c, int n, float tau, uint64_t *found, int *count) {
+    constexpr int kVec = FT == QMM_F32 ? 4 : 8, kWarps = kThreads / 32;
+    __shared__ int equal[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const float sorted = warp_sort_falling(most, lane);
-    maxima[warp][lane] = sorted;
-    if (threadIdx.x == 0) threads = count = 0;
-    if ((int)threadIdx.x < n) top[threadIdx.x] = 0;
+    const int64_t end = c.first + (int64_t)c.n * kVec;
     __syncthreads();
-    int rank = lane;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        // warp w's maxima that come before this one (equal ones: by warp)
-        int before = 0;
-#pragma unroll
-        for (int step = 16; step; step /= 2) {
-            const float v = maxima[w][before + step - 1];
-            before += v > sorted || (v == sorted && w < warp) ? step : 0;
+    if (threadIdx.x == 0) *count = 0;
+    __syncthreads();
+    for (int64_t e = c.first + threadIdx.x; e < end; e += kThreads) {
+        if (e < 0 || e >= c.V) continue;
+        const float x = load_one<FT>(c.row, e);
+        if (x > tau) {
+            const int at = atomicAdd(count, 1);
+            if (at < kFoundMax) found[at] = key_of(x, (uint32_t)e);
         }
-        const float v = maxima[w][before];
-        before += v > sorted || (v == sorted && w < warp) ? 1 : 0;
-        rank += w == warp ? 0 : before;
     }
-    if (rank == n - 1) tau_at = sorted;
     __syncthreads();
-    const float tau = tau_at;
-    if (most >= tau) reach[atomicAdd(&threads, 1)] = (int16_t)threadIdx.x;
-    __syncthreads();
-    for (int t = warp; t < threads; t += kThreads / 32)
-        for (int i = lane; i < c.vecs * kVec; i += 32) {
-            const int64_t e = c.first + ((int64_t)(i / kVec) * kThreads + reach[t]) * kVec + i % kVec;
-            if (e < 0 || e >= c.V) continue;
-            const float x = load_one<FT>(c.row, e);
-            if (x >= tau) {
-                const int at = atomicAdd(&count, 1);
-                if (at < kFoundMax) found[at] = key_of(x, (uint32_t)e);
-            }
-        }
-    __syncthreads();
-    const int all = count;
+    int all = *count;
     if (all > kFoundMax) return false;
-    if ((int)threadIdx.x < all) {
-        const uint64_t key = found[threadIdx.x];
-        int before = 0;
-        for (int i = 0; i < all; ++i) before += found[i] > key;
-        if (before < n) top[before] = key;
+    for (int64_t e0 = c.first; all < n && e0 < end; e0 += kThreads) {  // a CTA's width at a time
+        const int64_t e = e0 + threadIdx.x;
+        const bool is = e >= 0 && e < c.V && e < end && load_one<FT>(c.row, e) == tau;
+        const unsigned in_warp = __ballot_sync(0xffffffffu, is);
+        if (lane == 0) equal[warp] = __popc(in_warp);
+        __syncthreads();
+        int at = all + __popc(in_warp & ((1u << lane) - 1));
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) at += equal[w];
+            all += equal[w];
+        }
+        if (is && at < n) found[at] = key_of(tau, (uint32_t)e);
+        __syncthreads();
     }
+    // elements above tau may be more than n: all of them count
+    if (threadIdx.x == 0) *count = max(min(all, n), *count);
     __syncthreads();
     return true;
 }
 
+// -inf in every element of a word.
+template <int FT>
+__device__ constexpr uint32_t kNone = FT == QMM_F32 ? 0xFF800000u : FT == QMM_F16 ? 0xFC00FC00u : 0xFF80FF80u;
+
+// A vector that the row's start or end cuts: -inf for elements outside.
+template <int FT>
+__device__ __noinline__ uint4 cut_vector(const char *row, int64_t e, int64_t V) {
+    uint32_t w[4] = {kNone<FT>, kNone<FT>, kNone<FT>, kNone<FT>};
+#pragma unroll
+    for (int k = 0; k < (FT == QMM_F32 ? 4 : 8); ++k) {
+        if (e + k < 0 || e + k >= V) continue;
+        if (FT == QMM_F32) {
+            w[k % 4] = reinterpret_cast<const uint32_t *>(row)[e + k];
+        } else {
+            const uint32_t h = reinterpret_cast<const uint16_t *>(row)[e + k];
+            w[k / 2] = k % 2 ? __byte_perm(w[k / 2], h, 0x5410) : __byte_perm(w[k / 2], h, 0x3254);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int FT>
+__device__ __forceinline__ uint4 load_vector(const Chunk &c, int v) {
+    constexpr int kVec = FT == QMM_F32 ? 4 : 8;
+    const int64_t e = c.first + (int64_t)v * kVec;
+    if (e >= 0 && e + kVec <= c.V) return *reinterpret_cast<const uint4 *>(c.row + e * (16 / kVec));
+    return cut_vector<FT>(c.row, e, c.V);
+}
+
+// The larger of two words, element by element; NaN passed over.
+template <int FT>
+__device__ __forceinline__ uint32_t word_max(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if (FT == QMM_F32)
+        asm("max.f32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else if (FT == QMM_F16)
+        asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// The elements of a word: one, or two.
+template <int FT>
+__device__ __forceinline__ float2 word_values(uint32_t w) {
+    if (FT == QMM_F32) return make_float2(__uint_as_float(w), __uint_as_float(w));
+    if (FT == QMM_F16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
 // grid: rows x chunks. stats [row][chunk] and keys [row][chunk][top] where a
 // row has several chunks.
-template <int FT, int ELTS>
-__global__ void __launch_bounds__(kThreads, 3) logprobs_chunk_kernel(const Logprobs a, int chunks, Stats *stats, uint64_t *keys) {
-    constexpr int kVec = FT == QMM_F32 ? 4 : 8;
-    constexpr int kVecs = ELTS / kVec;
-    __shared__ float red[3][kThreads / 32];
-    __shared__ uint64_t best_of[2][kThreads / 32];
-    __shared__ uint64_t top[kTopMax];
+//
+// The chunk is read twice, the second time from L1, rather than held in
+// registers: 48 warps an SM instead of 24 hide the loads, and the code stays
+// within the instruction cache (unrolled over 64 registers: 280 us for 4096 x
+// 50001 bf16, a third of it waiting for instructions).
+//
+// Its largest keys: the W warps whose threads all hold elements give tau, the
+// smallest of their ceil(top / W)-th largest thread maxima. At least `top`
+// elements reach it, and few more do (top <= 8: 8 warps' smallest maximum,
+// about the 22nd largest element); they are collected while the exponentials
+// are summed, and rank themselves by counting. Where more reach tau than fit,
+// or there is a NaN, the functions above take over.
+template <int FT>
+__global__ void __launch_bounds__(kThreads, 6) logprobs_chunk_kernel(const Logprobs a, int chunks, Stats *stats, uint64_t *keys) {
+    constexpr int kVec = FT == QMM_F32 ? 4 : 8, kWarps = kThreads / 32;
+    __shared__ float red[3][kWarps], warp_tau[kWarps];
+    __shared__ uint64_t best_of[2][kWarps];
+    __shared__ uint64_t found[kFoundMax], top[kTopMax];
+    __shared__ int count;
     pdl_launch_dependents();
     pdl_wait();
     const int64_t row = blockIdx.x / chunks;
@@ -247,68 +287,79 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_chunk_kernel(const Logpr
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float inf = __int_as_float(0x7F800000);
 
-    // the chunk as 16-byte vectors of the row's aligned addresses; vectors
-    // that the row's ends cut are read element by element
-    constexpr int kSize = FT == QMM_F32 ? 4 : 2;
+    // the chunk as 16-byte vectors of the row's aligned addresses
     Chunk c;
-    c.row = static_cast<const char *>(a.X) + row * a.stride * kSize;
+    c.row = static_cast<const char *>(a.X) + row * a.stride * (16 / kVec);
     c.V = a.V;
-    c.first = (int64_t)chunk * kVecs * kThreads * kVec - (int)((uintptr_t)c.row % 16) / kSize;
-    const int64_t left = (a.V - c.first + kThreads * kVec - 1) / (kThreads * kVec);
-    c.vecs = left < kVecs ? (int)left : kVecs;  // the last chunk may hold few
-    float x[ELTS];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        const int64_t e = c.first + ((int64_t)i * kThreads + threadIdx.x) * kVec;
-        float *v = x + i * kVec;
-        if (i < c.vecs && e >= 0 && e + kVec <= a.V) {
-            const uint4 u = ld128(c.row + e * kSize);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (FT == QMM_F32) {
-                    v[k] = __uint_as_float(w[k]);
-                } else if (FT == QMM_F16) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
-                    v[(2 * k) % kVec] = f.x;
-                    v[(2 * k + 1) % kVec] = f.y;
-                } else {
-                    v[(2 * k) % kVec] = __uint_as_float(w[k] << 16);
-                    v[(2 * k + 1) % kVec] = __uint_as_float(w[k] & 0xFFFF0000u);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] = e + k >= 0 && e + k < a.V ? load_one<FT>(c.row, e + k) : -inf;
-        }
-    }
-    float mine = -inf;
-#pragma unroll
-    for (int i = 0; i < ELTS; ++i) mine = fmaxf(mine, x[i]);
+    const int skew = (int)((uintptr_t)c.row % 16) / (16 / kVec);
+    const int64_t vectors = (a.V + skew + kVec - 1) / kVec, v0 = vectors * chunk / chunks;
+    c.first = v0 * kVec - skew;
+    c.n = (int)(vectors * (chunk + 1) / chunks - v0);
 
-    // the chunk's sums
-    Stats s;
-    float most = mine;
-#pragma unroll
-    for (int d = 16; d; d /= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-    if (lane == 0) red[0][warp] = most;
+    uint32_t w_most = kNone<FT>, w_most2 = kNone<FT>;
+#pragma unroll 4
+    for (int v = threadIdx.x; v < c.n; v += kThreads) {
+        const uint4 u = load_vector<FT>(c, v);
+        w_most = word_max<FT>(w_most, word_max<FT>(u.x, u.y));
+        w_most2 = word_max<FT>(w_most2, word_max<FT>(u.z, u.w));
+    }
+    const float2 m2 = word_values<FT>(word_max<FT>(w_most, w_most2));
+    const float mine = fmaxf(m2.x, m2.y);
+    float most = warp_nth_largest(mine, 1);
+    const int full = min(c.n, kThreads) / 32;  // warps without an empty thread
+    const int nth = full ? (a.top + full - 1) / full : 0;
+    const float nth_most = warp < full && nth > 1 ? warp_nth_largest(mine, nth) : most;
+    if (lane == 0) {
+        red[0][warp] = most;
+        warp_tau[warp] = nth_most;
+    }
+    if (threadIdx.x == 0) count = 0;
     __syncthreads();
+    float tau = inf;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) most = fmaxf(most, red[0][w]);
+    for (int w = 0; w < kWarps; ++w) {
+        most = fmaxf(most, red[0][w]);
+        if (w < full) tau = fminf(tau, warp_tau[w]);
+    }
+    if (a.top == 1 && full) tau = most;
+    if (full == 0) tau = -inf;  // fewer than 32 vectors: all their elements fit
+    if (a.top == 0) tau = __int_as_float(0x7FC00000);  // nothing reaches a NaN
+
+    // the chunk's sums, and the elements that reach tau
+    Stats s;
     s.m = most == -inf ? 0.0f : most;
     uint64_t l2 = pair(0.0f, 0.0f), t2 = l2;
     const uint64_t minus = pair(-s.m, -s.m), log2e = pair(kLog2e, kLog2e);
+#pragma unroll 1
+    for (int v = threadIdx.x; v < c.n; v += kThreads) {
+        const uint4 u = load_vector<FT>(c, v);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        float x[kVec], reach = -inf;
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-        if (i < c.vecs)
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = word_values<FT>(w[k]);
+            x[FT == QMM_F32 ? k : (2 * k) % kVec] = f.x;
+            if (FT != QMM_F32) x[(2 * k + 1) % kVec] = f.y;
+        }
 #pragma unroll
-            for (int k = 0; k < kVec; k += 2) {
-                const uint64_t d = mul2(add2(pair(x[i * kVec + k], x[i * kVec + k + 1]), minus), log2e);
-                const float2 f = unpair(d);
-                const uint64_t e = pair(ex2(f.x), ex2(f.y));
-                l2 = add2(l2, e);
-                t2 = fma2(e, pair(fmaxf(f.x, -1000.0f), fmaxf(f.y, -1000.0f)), t2);  // 0, not 0 * -inf, where x = -inf
-            }
+        for (int k = 0; k < kVec; k += 2) {
+            const uint64_t d = mul2(add2(pair(x[k], x[k + 1]), minus), log2e);
+            const float2 f = unpair(d);
+            const uint64_t e = pair(ex2(f.x), ex2(f.y));
+            l2 = add2(l2, e);
+            t2 = fma2(e, pair(fmaxf(f.x, -1000.0f), fmaxf(f.y, -1000.0f)), t2);  // 0, not 0 * -inf, where x = -inf
+            reach = max3(reach, x[k], x[k + 1]);
+        }
+        if (reach >= tau) {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                if (x[k] >= tau) {
+                    const int at = atomicAdd(&count, 1);
+                    // the value and its place in the chunk; the key below
+                    if (at < kFoundMax) found[at] = (uint64_t)__float_as_uint(x[k]) << 32 | (uint32_t)(v * kVec + k);
+                }
+        }
+    }
     s.l = unpair(l2).x + unpair(l2).y;
     s.t = unpair(t2).x + unpair(t2).y;
 #pragma unroll
@@ -323,26 +374,49 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_chunk_kernel(const Logpr
     __syncthreads();
     s.l = s.t = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         s.l += red[1][w];
         s.t += red[2][w];
     }
 
-    // a NaN, which the maxima pass over, shows in the sum
-    if (a.top && (s.l != s.l || !largest_keys<FT>(c, a.top, mine, top))) largest_keys_by_rounds<FT>(c, a.top, top, best_of);
-    if (chunks == 1) {
-        finish_row<FT>(a, row, s, top);
-        return;
+    uint64_t *to = chunks == 1 ? top : keys + (int64_t)blockIdx.x * a.top;
+    if (threadIdx.x == 0 && chunks > 1) stats[blockIdx.x] = s;
+    if (a.top) {
+        const bool listed = count > kFoundMax;  // by the other function, as keys
+        // a NaN, which the maxima pass over, shows in the sum
+        if (s.l != s.l || (listed && !keys_above_and_equal<FT>(c, a.top, tau, found, &count))) {
+            largest_keys_by_rounds<FT>(c, a.top, to, best_of);
+        } else {
+            const int all = count;
+            uint64_t key = 0;
+            if ((int)threadIdx.x < all) {
+                key = found[threadIdx.x];
+                if (!listed) {  // -inf elements outside the row, where tau is -inf, have no key
+                    const int64_t e = c.first + (uint32_t)key;
+                    key = e >= 0 && e < a.V ? key_of(__uint_as_float((uint32_t)(key >> 32)), (uint32_t)e) : 0;
+                }
+            }
+            __syncthreads();
+            if ((int)threadIdx.x < all) found[threadIdx.x] = key;
+            if ((int)threadIdx.x < a.top) to[threadIdx.x] = 0;  // of a chunk of fewer elements
+            __syncthreads();
+            int before = 0;
+            if (key) {
+                for (int i = 0; i < all; ++i) before += found[i] > key;
+                if (before < a.top) to[before] = key;
+            }
+        }
     }
-    if (threadIdx.x == 0) stats[blockIdx.x] = s;
-    if ((int)threadIdx.x < a.top) keys[(int64_t)blockIdx.x * a.top + threadIdx.x] = top[threadIdx.x];
+    if (chunks > 1) return;
+    __syncthreads();
+    finish_row<FT>(a, row, s, top);
 }
 
 // One CTA joins a row's chunks: the sums, then the first `top` of the chunks'
 // falling lists by rounds of a maximum over the lists' heads.
 template <int FT>
 __global__ void __launch_bounds__(64) logprobs_join_kernel(const Logprobs a, int chunks, const Stats *stats, const uint64_t *keys) {
-    __shared__ uint64_t list[kListsMax * kTopMax];
+    extern __shared__ uint64_t list[];  // [chunks][top]
     __shared__ uint64_t top[kTopMax];
     pdl_launch_dependents();
     pdl_wait();
@@ -398,41 +472,38 @@ __global__ void __launch_bounds__(64) logprobs_join_kernel(const Logprobs a, int
     finish_row<FT>(a, row, s, top);
 }
 
-// Elements of a chunk and chunks of a row. Small chunks where the large ones
-// would not give every SM a CTA, as long as the join can hold their lists.
-struct Split {
-    int elts, chunks;
-};
-Split split_row(int64_t M, int64_t V) {
-    auto chunks = [&](int elts) { return (int)((V + 7 + kThreads * elts - 1) / (kThreads * elts)); };
-    if (M * chunks(kEltsLarge) < kSms && chunks(kEltsSmall) <= kSmallChunksMax) return {kEltsSmall, chunks(kEltsSmall)};
-    return {kEltsLarge, chunks(kEltsLarge)};
+// Chunks of a row: of about 32 KB, which six CTAs hold in an SM's L1, or of 8
+// KB where those would leave SMs idle, as long as the join can hold their lists.
+int chunks_of(int64_t M, int64_t V, int size) {
+    auto chunks = [&](int bytes) { return (int)((V * size + 15 + bytes - 1) / bytes); };
+    if (M * chunks(kChunkLarge) < 2 * kSms && chunks(kChunkSmall) <= kSmallChunksMax) return chunks(kChunkSmall);
+    return chunks(kChunkLarge);
 }
-static_assert((kVocabMax + 7) / (kThreads * kEltsLarge) + 1 <= kListsMax && kSmallChunksMax <= kListsMax, "join's lists");
+static_assert((kVocabMax * 4 + 15) / kChunkLarge + 1 <= kListsMax && kSmallChunksMax <= kListsMax, "join's lists");
+static_assert(kListsMax * kTopMax * 8 <= 48 * 1024, "join's shared memory");
 
 template <int FT>
-cudaError_t launch_typed(const Logprobs &a, Split sp, void *ws, cudaStream_t s) {
+cudaError_t launch_typed(const Logprobs &a, int chunks, void *ws, cudaStream_t s) {
     Stats *stats = static_cast<Stats *>(ws);
-    uint64_t *keys = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + align_up((size_t)a.M * sp.chunks * sizeof(Stats), 16));
-    auto kernel = sp.elts == kEltsLarge ? logprobs_chunk_kernel<FT, kEltsLarge> : logprobs_chunk_kernel<FT, kEltsSmall>;
-    const cudaError_t e = launch(kernel, dim3((unsigned)(a.M * sp.chunks)), kThreads, 0, s, a, sp.chunks, stats, keys);
-    if (e != cudaSuccess || sp.chunks == 1) return e;
-    return launch(logprobs_join_kernel<FT>, dim3((unsigned)a.M), 64, 0, s, a, sp.chunks, (const Stats *)stats, (const uint64_t *)keys);
+    uint64_t *keys = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + align_up((size_t)a.M * chunks * sizeof(Stats), 16));
+    const cudaError_t e = launch(logprobs_chunk_kernel<FT>, dim3((unsigned)(a.M * chunks)), kThreads, 0, s, a, chunks, stats, keys);
+    if (e != cudaSuccess || chunks == 1) return e;
+    return launch(logprobs_join_kernel<FT>, dim3((unsigned)a.M), 64, (size_t)chunks * a.top * 8, s, a, chunks, (const Stats *)stats, (const uint64_t *)keys);
 }
 
 }  // namespace
 
 size_t logprobs_bytes(int64_t M, int64_t V, int top) {
-    const Split sp = split_row(M, V);
-    if (sp.chunks == 1) return 0;
-    return align_up((size_t)M * sp.chunks * sizeof(Stats), 16) + (size_t)M * sp.chunks * top * 8;
+    const int c4 = chunks_of(M, V, 4), c2 = chunks_of(M, V, 2), chunks = c4 > c2 ? c4 : c2;  // for either size of logits
+    if (chunks == 1) return 0;
+    return align_up((size_t)M * chunks * sizeof(Stats), 16) + (size_t)M * chunks * top * 8;
 }
 
 cudaError_t launch_logprobs(const Logprobs &a, void *ws, cudaStream_t s) {
-    const Split sp = split_row(a.M, a.V);
-    if (a.ft == QMM_F32) return launch_typed<QMM_F32>(a, sp, ws, s);
-    if (a.ft == QMM_F16) return launch_typed<QMM_F16>(a, sp, ws, s);
-    return launch_typed<QMM_BF16>(a, sp, ws, s);
+    const int chunks = chunks_of(a.M, a.V, ftype_bytes(a.ft));
+    if (a.ft == QMM_F32) return launch_typed<QMM_F32>(a, chunks, ws, s);
+    if (a.ft == QMM_F16) return launch_typed<QMM_F16>(a, chunks, ws, s);
+    return launch_typed<QMM_BF16>(a, chunks, ws, s);
 }
 
 }  // namespace serving
