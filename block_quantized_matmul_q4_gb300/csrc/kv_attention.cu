@@ -18,7 +18,7 @@
 // decode step is reading the cache once; the MMAs run at a few percent of
 // their rate, which leaves room for exactness: Q and P are each two fp16
 // numbers (22 bits).
-#include "serving.cuh"
+#include "kv_attention.cuh"
 
 namespace qmm {
 namespace serving {
@@ -27,17 +27,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kStep = 16;        // tokens of a warp's step: one MMA tile of the cache
 constexpr int kPageBlock = 256;  // pages whose ids and scales are staged at once
-constexpr int kSplitTokens = kWarps * kStep;  // split boundaries
-// References: a new one gives its largest score the weight 2^11, and it is
-// renewed when a weight passes 2^15. fp16 holds weights up to 65504, so small
-// ones keep the most bits: two numbers resolve 2^-25, 2^-36 of the largest.
-constexpr float kTop = 11.0f, kRenew = 15.0f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+static_assert(kSplitTokens == kWarps * kStep, "a round of the warps' steps");
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -50,21 +40,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// Bytes 0 and 2 of x, signed codes, as two exact fp16 numbers: byte ^ 0x80
-// under the exponent of 1024 is 1152 + code.
-__device__ __forceinline__ uint32_t codes_02(uint32_t x) {
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(x), "r"(0x00FF00FFu), "r"(0x64806480u));  // (x & m) ^ c
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(d) : "r"(0x64806480u));
-    return d;
-}
-__device__ __forceinline__ uint32_t half_pair(float a, float b) { return pack_pair(QMM_F16, a, b); }
-// a and b less what half_pair(a, b) = h holds of them, as fp16.
-__device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t h) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    return half_pair(a - f.x, b - f.y);
-}
-
 // Bytes of a head that one lane loads, as the widest loads their alignment allows.
 template <int WORDS>
 __device__ __forceinline__ void load_words(const int8_t *p, uint32_t *w) {
@@ -84,47 +59,6 @@ __device__ __forceinline__ void load_words(const int8_t *p, uint32_t *w) {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) w[i] = ld32(p + 4 * i);
     }
-}
-
-// The rows of one work unit and the tokens that any of them sees.
-struct Tile {
-    Seq s;
-    int b, r0, rows;       // rows r0 .. r0 + rows - 1 of the sequence's n * group
-    int start;             // position of the sequence's first row
-    int lo, hi;            // tokens, lo a multiple of 16
-};
-__device__ __forceinline__ Tile tile_of(const Batch &g, const Attend &a, int page, int group, int tile_rows, int64_t unit) {
-    Tile t;
-    const Unit u = find_unit(unit, g.batch, [&](int b) { return (seq_at(g, b, page).n * group + tile_rows - 1) / tile_rows; });
-    t.b = u.b;
-    if (u.b < 0) return t;
-    t.s = seq_at(g, u.b, page);
-    t.r0 = u.i * tile_rows;
-    t.rows = min(tile_rows, t.s.n * group - t.r0);
-    t.start = t.s.len - t.s.n;
-    const int first = t.start + t.r0 / group, last = t.start + (t.r0 + t.rows - 1) / group;
-    t.hi = a.causal ? last + 1 : t.s.len;
-    t.lo = a.window && a.window <= first ? (int)(first - a.window + 1) & ~15 : 0;
-    return t;
-}
-// Splits of a tile's tokens: each `chunk` tokens, the last one the rest.
-__device__ __forceinline__ int splits_of(const Tile &t, int chunk, int splits) {
-    return max(1, min(splits, (t.hi - t.lo + chunk - 1) / chunk));
-}
-
-// Writes a row's result from its joined sums: o / l and the log sum.
-__device__ __forceinline__ void write_lse(const Attend &a, int64_t at, float m, float l) {
-    if (a.lse) a.lse[at] = l == 0.0f ? __int_as_float(0xFF800000) : (m + log2f(l)) * 0.693147180559945f;
-}
-__device__ __forceinline__ void write_out(const Attend &a, int64_t at, float4 o, float l) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    if (a.ft == QMM_F32)
-        store4<QMM_F32>(a.out, at, o);
-    else if (a.ft == QMM_F16)
-        store4<QMM_F16>(a.out, at, o);
-    else
-        store4<QMM_BF16>(a.out, at, o);
 }
 
 // Shared memory: the staged pages, then rotated Q (fp32), whose place the
@@ -183,8 +117,7 @@ __global__ void __launch_bounds__(kThreads)
 
     // Q as the B operand: lane (lg, lt) holds row lg, and of k step s the four
     // elements that its K words hold, (0, 2) and (1, 3) paired as codes_02
-    // pairs them. Each row times a power of two that puts its largest
-    // element in [2^13, 2^14).
+    // pairs them.
     uint32_t qh[NT][kSteps][2], ql[NT][kSteps][2];
     float qf[NT][2];  // rows 2 lt, 2 lt + 1 of a tile: what undoes that, times the scale
 #pragma unroll
@@ -198,10 +131,8 @@ __global__ void __launch_bounds__(kThreads)
         }
         most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
         most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        // 2^(13 - floor(log2 most)), within fp32's normal numbers; 1 for 0 and non-finite rows
-        const int e = (int)(most >> 23);
-        const int be = e == 0 || e == 255 ? 127 : min(127 + 13 + 127 - e, 253);
-        const float up = __int_as_float(be << 23), down = __int_as_float((254 - be) << 23);
+        const float2 rs = row_scale(most);
+        const float up = rs.x, down = rs.y;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const float4 v = *reinterpret_cast<const float4 *>(&qs[8 * n + lg][16 * kKWords * (s / kKWords) + 4 * kKWords * lt + 4 * (s % kKWords)]);
@@ -438,19 +369,15 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// How a call is split: rows of a tile, upper bound of tiles, tokens and
-// number of splits.
-struct Plan {
-    int tile_rows;
-    int64_t units;
-    int chunk, splits;
-};
+// Rows of a sequence up to which a tile is eight or sixteen of them.
+constexpr int64_t kFewRows = 64;
 Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv, int64_t window) {
     Plan p;
     const int64_t group = q_heads / heads;
     // Sixteen rows where eight do not hold a sequence's: the cache is then
     // read half as often. From 192 elements a head their registers do not fit.
-    p.tile_rows = dim <= 128 && group * (max_q > 1 ? max_q : 1) > 8 ? 16 : 8;
+    const int64_t rows = group * (max_q > 1 ? max_q : 1);  // of the longest sequence
+    p.tile_rows = rows > kFewRows ? kPrefillRows : dim <= 128 && rows > 8 ? 16 : 8;
     const int64_t seqs = T < batch ? T : batch;
     p.units = T * group / p.tile_rows + seqs;
     const int64_t tiles = (T * group + p.tile_rows - 1) / p.tile_rows;  // about as many have rows
@@ -492,7 +419,9 @@ cudaError_t launch_kv_attention(const Cache &c, const Batch &g, const Rope &r, c
     float *part = static_cast<float *>(ws);
     cudaError_t e;
     const bool wide = p.tile_rows == 16;
-    switch (c.dim) {
+    if (p.tile_rows == kPrefillRows)
+        e = launch_kv_prefill(c, g, r, a, p, part, s);
+    else switch (c.dim) {
     case 64: e = wide ? launch_tiles<64, 2>(c, g, r, a, p, part, s) : launch_tiles<64, 1>(c, g, r, a, p, part, s); break;
     case 96: e = wide ? launch_tiles<96, 2>(c, g, r, a, p, part, s) : launch_tiles<96, 1>(c, g, r, a, p, part, s); break;
     case 128: e = wide ? launch_tiles<128, 2>(c, g, r, a, p, part, s) : launch_tiles<128, 1>(c, g, r, a, p, part, s); break;

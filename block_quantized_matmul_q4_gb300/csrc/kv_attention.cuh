@@ -1,0 +1,100 @@
+// kv_attention.cuh -- what the attention kernels share: codes as fp16, work
+// tiles, splits of a sequence's tokens and results.
+#pragma once
+
+#include "serving.cuh"
+
+namespace qmm {
+namespace serving {
+
+// References: a new one gives its largest score the weight 2^11, and it is
+// renewed when a weight passes 2^15. fp16 holds weights up to 65504, so small
+// ones keep the most bits: two numbers resolve 2^-25, 2^-36 of the largest.
+constexpr float kTop = 11.0f, kRenew = 15.0f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Bytes 0 and 2 of x, signed codes, as two exact fp16 numbers: byte ^ 0x80
+// under the exponent of 1024 is 1152 + code.
+__device__ __forceinline__ uint32_t codes_02(uint32_t x) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(x), "r"(0x00FF00FFu), "r"(0x64806480u));  // (x & m) ^ c
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(d) : "r"(0x64806480u));
+    return d;
+}
+__device__ __forceinline__ uint32_t half_pair(float a, float b) { return pack_pair(QMM_F16, a, b); }
+// a and b less what half_pair(a, b) = h holds of them, as fp16.
+__device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return half_pair(a - f.x, b - f.y);
+}
+
+// A row of Q goes into fp16 times a power of two that puts its largest
+// element (`most`: the bits of its magnitude) in [2^13, 2^14): {that power,
+// its inverse}, both normal fp32 numbers; 1 for a row of zeros or one that is
+// not finite.
+__device__ __forceinline__ float2 row_scale(uint32_t most) {
+    const int e = (int)(most >> 23);
+    const int up = e == 0 || e >= 255 ? 127 : min(127 + 13 + 127 - e, 253);
+    return make_float2(__int_as_float(up << 23), __int_as_float((254 - up) << 23));
+}
+
+// The rows of one work unit and the tokens that any of them sees.
+struct Tile {
+    Seq s;
+    int b, r0, rows;       // rows r0 .. r0 + rows - 1 of the sequence's n * group
+    int start;             // position of the sequence's first row
+    int lo, hi;            // tokens, lo a multiple of 16
+};
+__device__ __forceinline__ Tile tile_of(const Batch &g, const Attend &a, int page, int group, int tile_rows, int64_t unit) {
+    Tile t;
+    const Unit u = find_unit(unit, g.batch, [&](int b) { return (seq_at(g, b, page).n * group + tile_rows - 1) / tile_rows; });
+    t.b = u.b;
+    if (u.b < 0) return t;
+    t.s = seq_at(g, u.b, page);
+    t.r0 = u.i * tile_rows;
+    t.rows = min(tile_rows, t.s.n * group - t.r0);
+    t.start = t.s.len - t.s.n;
+    const int first = t.start + t.r0 / group, last = t.start + (t.r0 + t.rows - 1) / group;
+    t.hi = a.causal ? last + 1 : t.s.len;
+    t.lo = a.window && a.window <= first ? (int)(first - a.window + 1) & ~15 : 0;
+    return t;
+}
+// Splits of a tile's tokens: each `chunk` tokens, the last one the rest.
+__device__ __forceinline__ int splits_of(const Tile &t, int chunk, int splits) {
+    return max(1, min(splits, (t.hi - t.lo + chunk - 1) / chunk));
+}
+
+// Writes a row's result from its joined sums: o / l and the log sum.
+__device__ __forceinline__ void write_lse(const Attend &a, int64_t at, float m, float l) {
+    if (a.lse) a.lse[at] = l == 0.0f ? __int_as_float(0xFF800000) : (m + log2f(l)) * 0.693147180559945f;
+}
+__device__ __forceinline__ void write_out(const Attend &a, int64_t at, float4 o, float l) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (a.ft == QMM_F32)
+        store4<QMM_F32>(a.out, at, o);
+    else if (a.ft == QMM_F16)
+        store4<QMM_F16>(a.out, at, o);
+    else
+        store4<QMM_BF16>(a.out, at, o);
+}
+
+// How a call is split: rows of a tile, upper bound of tiles, tokens and
+// number of splits.
+struct Plan {
+    int tile_rows;
+    int64_t units;
+    int chunk, splits;
+};
+constexpr int kSplitTokens = 64;  // splits begin at multiples of this
+constexpr int kPrefillRows = 128;
+
+cudaError_t launch_kv_prefill(const Cache &c, const Batch &g, const Rope &r, const Attend &a, const Plan &p, float *part,
+                              cudaStream_t s);
+
+}  // namespace serving
+}  // namespace qmm
