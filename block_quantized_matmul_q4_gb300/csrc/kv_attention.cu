@@ -369,9 +369,12 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// Tokens that the tensor cores may sum for an fp32 output.
+constexpr int64_t kSumTokens = 1024;
 // Rows of a sequence up to which a tile is eight or sixteen of them.
 constexpr int64_t kFewRows = 64;
-Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv, int64_t window) {
+Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv, int64_t window,
+             int ft) {
     Plan p;
     const int64_t group = q_heads / heads;
     // Sixteen rows where eight do not hold a sequence's: the cache is then
@@ -389,6 +392,7 @@ Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_
     const int64_t most = (kv + kSplitTokens - 1) / kSplitTokens;
     if (splits > most) splits = most;
     if (splits > 256) splits = 256;
+    if (p.tile_rows == kPrefillRows && ft == QMM_F32 && splits < (kv + kSumTokens - 1) / kSumTokens) splits = (kv + kSumTokens - 1) / kSumTokens;
     p.chunk = (int)(((kv + splits - 1) / splits + kSplitTokens - 1) / kSplitTokens * kSplitTokens);
     p.splits = (int)((kv + p.chunk - 1) / p.chunk);
     return p;
@@ -410,12 +414,12 @@ cudaError_t launch_tiles(const Cache &c, const Batch &g, const Rope &r, const At
 size_t kv_attention_bytes(int heads, int dim, int page, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv) {
     (void)page;
     // for any window: a window only lowers the number of splits' tokens, not their bound
-    const Plan p = plan_of(heads, dim, batch, q_heads, T, max_q, max_kv, 0);
+    const Plan p = plan_of(heads, dim, batch, q_heads, T, max_q, max_kv, 0, QMM_F32);
     return p.splits == 1 ? 0 : (size_t)p.units * heads * p.splits * p.tile_rows * (dim + 4) * 4;
 }
 
 cudaError_t launch_kv_attention(const Cache &c, const Batch &g, const Rope &r, const Attend &a, void *ws, cudaStream_t s) {
-    const Plan p = plan_of(c.heads, c.dim, g.batch, a.q_heads, g.T, a.max_q, a.max_kv, a.window);
+    const Plan p = plan_of(c.heads, c.dim, g.batch, a.q_heads, g.T, a.max_q, a.max_kv, a.window, a.ft);
     float *part = static_cast<float *>(ws);
     cudaError_t e;
     const bool wide = p.tile_rows == 16;

@@ -14,7 +14,9 @@
 // that the tensor cores work for one while the other waits for its softmax.
 //
 // O stays in TMEM; a row whose reference is renewed (a weight would pass
-// 2^15) has it multiplied there, which is rare.
+// 2^15) has it multiplied there, which is rare. The tensor cores cut their
+// sums off rather than round them, which 8192 tokens add up to 1.7e-5 of the
+// result: for fp32 outputs a call is split so that no O sums more than 1024.
 #include "kv_attention.cuh"
 #include "tc.cuh"
 
@@ -72,6 +74,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+// Waits for the thread's TMEM loads. Their results pass through, so that no
+// use of them is scheduled before the wait.
+__device__ __forceinline__ void ld_wait16(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                   "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :
+                 : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -177,7 +188,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
         if (lane == 0) {
             constexpr uint32_t idesc_s = tc::idesc_f16_f32(kRows, kTok), idesc_o = tc::idesc_f16_f32(kRows, D);
             const uint64_t qd = tc::smem_desc(q_at, 1024, 2), kd = tc::smem_desc(k_at, 1024, 2), vd = tc::smem_desc(v_at, 1024, 2);
+            // Tile i's scores go where the weights of tile i - 2 lie: those must
+            // have been used (MMAs of different shapes keep no order).
             auto scores = [&](int i) {
+                if (i > 1 && !mbar_wait(smem_u32(&tail->pv_done), (uint32_t)(i & 1), g.err)) return false;
                 if (!mbar_wait(smem_u32(&tail->k_full), (uint32_t)(i & 1), g.err)) return false;
                 tc::fence_after_sync();
                 for (int p = 0; p < q_parts; ++p)
@@ -330,6 +344,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
         const int to = r >= t.rows ? 0 : a.causal ? pos + 1 : t.s.len;
         const float qf = tail->down[r] * a.scale;
         float m = -inf, l = 0.0f;
+        const int64_t at = (int64_t)(t.s.row0 + (t.r0 + r) / group) * a.q_heads + h * group + (t.r0 + r) % group;
+        float *const to_part = part + (((unit * c.heads + h) * gridDim.z + blockIdx.z) * kRows + r) * (D + 4);
         // lane q < 4: the scales of the tile's tokens 16 q .. 16 q + 15 (one page)
         const int32_t *ids = g.table + (int64_t)t.b * g.max_pages;
         float ks = 0.0f, vs = 0.0f;
@@ -363,12 +379,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
             const bool all = __all_sync(0xffffffffu, t0 >= from && t0 + kTok <= to);
             ok = mbar_wait_warp(smem_u32(&tail->s_full[i & 1]), (uint32_t)((i >> 1) & 1), g.err);
             if (!ok) break;
+            __syncwarp();
             tc::fence_after_sync();
             const uint32_t sp = lanes + (i & 1) * kTok;
             float x[kTok];
 #pragma unroll
             for (int q = 0; q < 4; ++q) tc::tmem_ld16(sp + 16 * q, *reinterpret_cast<float(*)[16]>(&x[16 * q]));
-            tc::tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ld_wait16(*reinterpret_cast<float(*)[16]>(&x[16 * q]));
             // u = x f + lv, the largest one that the row sees
             float most = -inf;
 #pragma unroll
@@ -392,15 +410,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
                 m = n;
                 l *= scale;
                 if (i > 0) {
+                    // S(i) came after tile i - 2's values, so at most tile i - 1's are open
                     ok = mbar_wait_warp(smem_u32(&tail->pv_done), (uint32_t)((i - 1) & 1), g.err);
                     if (!ok) break;
+                    __syncwarp();
                     tc::fence_after_sync();
 #pragma unroll 1
                     for (int d = 0; d < D; d += 16) {
                         float o[16];
                         uint32_t w[16];
                         tc::tmem_ld16(lanes + S::kTmemO + d, o);
-                        tc::tmem_ld_wait();
+                        ld_wait16(o);
 #pragma unroll
                         for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * scale);
                         tc::tmem_st16(lanes + S::kTmemO + d, w);
@@ -423,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
                 }
                 l = fmaf(unpair(sum).x + unpair(sum).y, iv[q], l);
             }
+            __syncwarp();
             tc::tmem_st16(sp, *reinterpret_cast<uint32_t(*)[16]>(&hi[0]));
             tc::tmem_st16(sp + 16, *reinterpret_cast<uint32_t(*)[16]>(&hi[16]));
             if (PARTS == 2) {
@@ -433,17 +454,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
             tc::fence_before_sync();
             mbar_arrive(smem_u32(&tail->p_full[i & 1]));
         }
-        if (ok) ok = mbar_wait_warp(smem_u32(&tail->pv_done), (uint32_t)((tiles - 1) & 1), g.err);
+        // (not pv_done: two of its phases may be open here)
+        if (ok) ok = mbar_wait_warp(smem_u32(&tail->done), 0, g.err);
         if (ok) {
             tc::fence_after_sync();
-            const int row = t.s.row0 + (t.r0 + r) / group, head = h * group + (t.r0 + r) % group;
-            const int64_t at = (int64_t)row * a.q_heads + head;
-            float *to_part = part + (((unit * c.heads + h) * gridDim.z + blockIdx.z) * kRows + r) * (D + 4);
 #pragma unroll 1
             for (int d = 0; d < D; d += 16) {
                 float o[16];
                 tc::tmem_ld16(lanes + S::kTmemO + d, o);
-                tc::tmem_ld_wait();
+                ld_wait16(o);
                 if (r < t.rows) {
 #pragma unroll
                     for (int k = 0; k < 16; k += 4) {

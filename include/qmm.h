@@ -496,8 +496,8 @@ qmm_status qmm_kv_read(const qmm_kv_cache *cache, const int32_t *pages, int64_t 
  * the tokens j <= p, with window > 0 only those j > p - window, with causal
  * == 0 every token of its sequence:
  *   x_j = scale * (q . k_j),  lse = log sum_j e^x_j,  out = sum_j e^(x_j - lse) v_j
- * out: [T][q_heads][head_dim] contiguous, type qt, 16-byte aligned; lse: fp32
- * [T][q_heads] or NULL. A row that sees nothing gives out = 0, lse = -inf.
+ * out: [T][q_heads][head_dim] contiguous, type qt, 16-byte aligned, not
+ * overlapping Q or the cache; lse: fp32 [T][q_heads] or NULL. A row that sees nothing gives out = 0, lse = -inf.
  * Arithmetic: the codes are exact in fp16; q is taken as a sum of two fp16
  * numbers times a power of two per row and head (22 bits), the
  * probabilities as two fp16 numbers where qt is fp32 or the call is a decode
