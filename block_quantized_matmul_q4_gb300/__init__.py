@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -34,6 +35,7 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_st = ctypes.c_char_p  # a structure of include/qmm.h, packed into bytes
 _SIGS = {
     "qmm_block_bytes": (_sz, [_i32]),
     "qmm_block_elems": (_i32, [_i32]),
@@ -57,10 +59,10 @@ _SIGS = {
     "qmm_w4a16": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp]),
     "qmm_w4a16_lut": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp]),
     "qmm_w4a16_unpack_zeros": (_i32, [_vp, _vp, _i64, _i64, _vp]),
-    "qmm_kv_append": (_i32, [_vp, _vp, _vp, _i32, _vp, _i64, _vp, _i64, _i64, _vp]),
-    "qmm_kv_read": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _vp]),
-    "qmm_kv_attention_workspace_bytes": (_sz, [_vp, _i32, _i32, _i64, _i64, _i64]),
-    "qmm_kv_attention": (_i32, [_vp, _vp, _vp, _i32, _vp, _i64, _i64, _i32, ctypes.c_float, _i32, _i64, _i64, _i64,
+    "qmm_kv_append": (_i32, [_st, _st, _st, _i32, _vp, _i64, _vp, _i64, _i64, _vp]),
+    "qmm_kv_read": (_i32, [_st, _vp, _i64, _i32, _vp, _vp, _vp]),
+    "qmm_kv_attention_workspace_bytes": (_sz, [_st, _i32, _i32, _i64, _i64, _i64]),
+    "qmm_kv_attention": (_i32, [_st, _st, _st, _i32, _vp, _i64, _i64, _i32, ctypes.c_float, _i32, _i64, _i64, _i64,
                                 _vp, _vp, _vp, _sz, _vp]),
     "qmm_logprobs_workspace_bytes": (_sz, [_i64, _i64, _i32]),
     "qmm_logprobs": (_i32, [_i32, _vp, _i64, _i64, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -91,8 +93,14 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream and _device:  # torch's current stream without its Python object (3 us)
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -261,7 +269,9 @@ def _ftype(t) -> int:
 
 
 def _typed(t, dtype, what: str):
-    if t is not None and t.dtype != dtype:
+    if t is None:
+        return None
+    if t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
     return _ptr(t)
 
@@ -270,50 +280,58 @@ def _heads(t, dim: int, what: str):
     """(pointer, row stride) of [rows][heads][dim] rows whose heads are contiguous."""
     if not t.is_cuda:
         raise ValueError("libqmm takes device tensors")
-    if t.dim() != 3 or t.size(2) != dim or (t.numel() and (t.stride(2) != 1 or (t.size(1) > 1 and t.stride(1) != dim))):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != dim or (shape[0] and (stride[2] != 1 or (shape[1] > 1 and stride[1] != dim))):
         raise ValueError(f"{what} must be [rows][heads][{dim}] with contiguous heads")
-    return t.data_ptr(), t.stride(0) if t.size(0) > 1 else max(t.stride(0), t.size(1) * dim)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], shape[1] * dim)
 
 
-class KvCache(ctypes.Structure):
+class KvCache:
     """qmm_kv_cache over tensors: codes k, v int8 [pages][heads][page_tokens][head_dim],
     scales fp32 [pages][heads]. The tensors are kept alive."""
-    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_pages", _i64), ("heads", _i32),
-                ("page_tokens", _i32), ("head_dim", _i32)]
+    __slots__ = ("raw", "tensors", "num_pages", "heads", "page_tokens", "head_dim")
+    _pack = struct.Struct("@PPPPqiii4x").pack
 
     def __init__(self, k, v, k_scale, v_scale):
-        if k.dim() != 4 or v.shape != k.shape or k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2]:
+        shape = k.shape
+        if len(shape) != 4 or v.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
             raise ValueError("k and v must be [pages][heads][page_tokens][head_dim], the scales [pages][heads]")
-        super().__init__(_typed(k, torch.int8, "k"), _typed(v, torch.int8, "v"), _typed(k_scale, torch.float32, "k_scale"),
-                         _typed(v_scale, torch.float32, "v_scale"), *k.shape)
+        self.num_pages, self.heads, self.page_tokens, self.head_dim = shape
+        self.raw = self._pack(_typed(k, torch.int8, "k"), _typed(v, torch.int8, "v"), _typed(k_scale, torch.float32, "k_scale"),
+                              _typed(v_scale, torch.float32, "v_scale"), *shape)
         self.tensors = (k, v, k_scale, v_scale)
 
 
-class KvBatch(ctypes.Structure):
+class KvBatch:
     """qmm_kv_batch over int32 tensors: table [batch][max_pages], first [batch + 1], length [batch]."""
-    _fields_ = [("table", _vp), ("first", _vp), ("length", _vp), ("batch", _i32), ("max_pages", _i32)]
+    __slots__ = ("raw", "tensors", "batch", "max_pages")
+    _pack = struct.Struct("@PPPii").pack
 
     def __init__(self, table, first, length):
-        if table.dim() != 2 or first.shape != (table.size(0) + 1,) or length.shape != (table.size(0),):
+        shape = table.shape
+        if len(shape) != 2 or first.shape != (shape[0] + 1,) or length.shape != (shape[0],):
             raise ValueError("table must be [batch][max_pages], first [batch + 1], length [batch]")
-        super().__init__(_typed(table, torch.int32, "table"), _typed(first, torch.int32, "first"),
-                         _typed(length, torch.int32, "length"), *table.shape)
+        self.batch, self.max_pages = shape
+        self.raw = self._pack(_typed(table, torch.int32, "table"), _typed(first, torch.int32, "first"),
+                              _typed(length, torch.int32, "length"), *shape)
         self.tensors = (table, first, length)
 
 
-class Rope(ctypes.Structure):
+class Rope:
     """qmm_rope over an fp32 tensor [positions][dim / 2][2] of (cos, sin)."""
-    _fields_ = [("table", _vp), ("rows", _i64), ("dim", _i32), ("adjacent", _i32)]
+    __slots__ = ("raw", "tensors")
+    _pack = struct.Struct("@Pqii").pack
 
     def __init__(self, table, adjacent: bool = False):
-        if table.dim() != 3 or table.size(2) != 2:
+        shape = table.shape
+        if len(shape) != 3 or shape[2] != 2:
             raise ValueError("table must be [positions][dim / 2][2]")
-        super().__init__(_typed(table, torch.float32, "table"), table.size(0), 2 * table.size(1), int(adjacent))
+        self.raw = self._pack(_typed(table, torch.float32, "table"), shape[0], 2 * shape[1], int(adjacent))
         self.tensors = (table,)
 
 
-def _ref(s):
-    return None if s is None else ctypes.addressof(s)
+def _raw(s):
+    return None if s is None else s.raw
 
 
 def empty_kv_cache(num_pages: int, heads: int, page_tokens: int, head_dim: int, device="cuda") -> KvCache:
@@ -327,10 +345,11 @@ def qmm_kv_append(cache: KvCache, batch: KvBatch, rope, K, V, stream=None):
     rotated by `rope` (a Rope or None) on the way; see include/qmm.h."""
     k, ks = _heads(K, cache.head_dim, "K")
     v, vs = _heads(V, cache.head_dim, "V")
-    if V.shape != K.shape or V.dtype != K.dtype or K.size(1) != cache.heads:
+    rows, heads, _ = K.shape
+    if V.shape != K.shape or V.dtype != K.dtype or heads != cache.heads:
         raise ValueError("K and V must have one type, the same rows and the cache's heads")
     _check("qmm_kv_append",
-           _lib.qmm_kv_append(_ref(cache), _ref(batch), _ref(rope), _ftype(K), k, ks, v, vs, K.size(0), _stream(stream)))
+           _lib.qmm_kv_append(cache.raw, batch.raw, _raw(rope), _ftype(K), k, ks, v, vs, rows, _stream(stream)))
 
 
 def qmm_kv_read(cache: KvCache, pages, K, V, stream=None):
@@ -339,12 +358,12 @@ def qmm_kv_read(cache: KvCache, pages, K, V, stream=None):
     if K.shape != shape or V.shape != shape or K.dtype != V.dtype:
         raise ValueError(f"K and V must be {shape} of one type")
     _check("qmm_kv_read",
-           _lib.qmm_kv_read(_ref(cache), _typed(pages, torch.int32, "pages"), shape[0], _ftype(K), _ptr(K), _ptr(V),
+           _lib.qmm_kv_read(cache.raw, _typed(pages, torch.int32, "pages"), shape[0], _ftype(K), _ptr(K), _ptr(V),
                             _stream(stream)))
 
 
 def qmm_kv_attention_workspace_bytes(cache: KvCache, batch: int, q_heads: int, T: int, max_q: int, max_kv: int) -> int:
-    return int(_lib.qmm_kv_attention_workspace_bytes(_ref(cache), batch, q_heads, T, max_q, max_kv))
+    return int(_lib.qmm_kv_attention_workspace_bytes(cache.raw, batch, q_heads, T, max_q, max_kv))
 
 
 def qmm_kv_attention(cache: KvCache, batch: KvBatch, rope, Q, out, lse=None, *, scale: float, causal: bool = True,
@@ -353,10 +372,11 @@ def qmm_kv_attention(cache: KvCache, batch: KvBatch, rope, Q, out, lse=None, *, 
     [T][q_heads] their log sums; max_q and max_kv are the most rows and the
     largest length of any sequence; see include/qmm.h."""
     q, stride = _heads(Q, cache.head_dim, "Q")
-    if out.shape != Q.shape or out.dtype != Q.dtype or (lse is not None and lse.shape != Q.shape[:2]):
+    shape = Q.shape
+    if out.shape != shape or out.dtype != Q.dtype or (lse is not None and lse.shape != shape[:2]):
         raise ValueError("out must be like Q, lse [rows][q_heads]")
     _check("qmm_kv_attention",
-           _lib.qmm_kv_attention(_ref(cache), _ref(batch), _ref(rope), _ftype(Q), q, stride, Q.size(0), Q.size(1), scale,
+           _lib.qmm_kv_attention(cache.raw, batch.raw, _raw(rope), _ftype(Q), q, stride, shape[0], shape[1], scale,
                                  int(causal), window, max_q, max_kv, _ptr(out), _typed(lse, torch.float32, "lse"),
                                  _ptr(workspace), ws_bytes, _stream(stream)))
 
@@ -372,17 +392,18 @@ def qmm_logprobs(X, given=None, lse=None, entropy=None, given_logp=None, top_ids
     their top_logp [M][top]; None where not wanted; see include/qmm.h."""
     if not X.is_cuda:
         raise ValueError("libqmm takes device tensors")
-    if X.dim() != 2 or (X.size(1) > 1 and X.stride(1) != 1):
+    shape, stride = X.shape, X.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError("X must be [M][V] with contiguous rows")
-    M, V = X.shape
-    G = 0 if given is None else given.numel() // M if M else 0
-    top = 0 if top_ids is None else top_ids.numel() // M if M else 0
+    M, V = shape
+    G = given.numel() // M if given is not None and M else 0
+    top = top_ids.numel() // M if top_ids is not None and M else 0
     for t, n, what in ((given, G, "given"), (given_logp, G, "given_logp"), (top_ids, top, "top_ids"), (top_logp, top, "top_logp"),
                        (lse, 1, "lse"), (entropy, 1, "entropy")):
         if t is not None and t.numel() != M * n:
             raise ValueError(f"{what} must hold {n} values for each of the {M} rows")
     _check("qmm_logprobs",
-           _lib.qmm_logprobs(_ftype(X), X.data_ptr(), X.stride(0) if M > 1 else max(X.stride(0), V), M, V,
+           _lib.qmm_logprobs(_ftype(X), X.data_ptr(), stride[0] if M > 1 else max(stride[0], V), M, V,
                              _typed(given, torch.int32, "given"), G, top, _typed(lse, torch.float32, "lse"),
                              _typed(entropy, torch.float32, "entropy"), _typed(given_logp, torch.float32, "given_logp"),
                              _typed(top_ids, torch.int32, "top_ids"), _typed(top_logp, torch.float32, "top_logp"),
