@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kStep = 16;        // tokens of a warp's step: one MMA tile of the cache
+constexpr int kAhead = 2;        // steps between a prefetch and its use
 constexpr int kPageBlock = 256;  // pages whose ids and scales are staged at once
 static_assert(kSplitTokens == kWarps * kStep, "a round of the warps' steps");
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -34,12 +35,31 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same onto zeros.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// a + b in pairs: one instruction for two.
+__device__ __forceinline__ void add_pairs(float (&a)[4], const float (&b)[4]) {
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%6, %7};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%2, %3}, x;\n\t}"
+        : "+f"(a[0]), "+f"(a[1]), "+f"(a[2]), "+f"(a[3])
+        : "f"(b[0]), "f"(b[1]), "f"(b[2]), "f"(b[3]));
+}
 // An 8 x 8 matrix of 16-bit elements, two of a row per lane, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+__device__ __forceinline__ void prefetch_l2(const void *p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // Bytes of a head that one lane loads, as the widest loads their alignment allows.
 template <int WORDS>
 __device__ __forceinline__ void load_words(const int8_t *p, uint32_t *w) {
@@ -61,6 +81,29 @@ __device__ __forceinline__ void load_words(const int8_t *p, uint32_t *w) {
     }
 }
 
+// Part (m, l, o) joined to another: both relative to the larger reference. A
+// part without a reference holds zeros, or the NaN of a poisoned page.
+__device__ __forceinline__ void join_part(float &m, float &l, float4 &o, float pm, float pl, float4 p) {
+    const float inf = __int_as_float(0x7F800000), n = fmaxf(m, pm);
+    const float f = m == -inf ? 0.0f : ex2(m - n), g = pm == -inf ? 0.0f : ex2(pm - n);
+    l = fmaf(g, pl, f * l);
+    o = make_float4(fmaf(g, p.x, f * o.x), fmaf(g, p.y, f * o.y), fmaf(g, p.z, f * o.z), fmaf(g, p.w, f * o.w));
+    m = n;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes at this CTA's shared address `at` in the cluster's CTA `rank`.
+__device__ __forceinline__ float4 peer_load(uint32_t at, int rank) {
+    float4 v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at), "r"(rank)
+                 : "memory");
+    return v;
+}
+
 // Shared memory: the staged pages, then rotated Q (fp32), whose place the
 // warps' results take at the end.
 template <int D, int NT>
@@ -68,12 +111,15 @@ struct Smem {
     int id[kPageBlock];
     float ks[kPageBlock], lv[kPageBlock], iv[kPageBlock];  // K scale, log2 and inverse of the V scale
     float ml[2][kWarps][8 * NT];
+    __align__(16) float2 all[8 * NT];  // a row's reference and sum over the warps
     float o[kWarps][8 * NT][D + 4];
 };
 
-// grid: (units of 8 * NT rows, cached heads, splits).
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads)
+// grid: (units of 8 * NT rows, cached heads, splits). CLUSTER: the splits of a
+// unit are a cluster and join through its shared memory; otherwise, with
+// several splits, through `part` and a second kernel.
+template <int D, int NT, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, D <= 128 && NT == 1 ? 4 : 1)
     kv_attention_kernel(const Cache c, const Batch g, const Rope rope, const Attend a, int chunk, float *part) {
     constexpr int kRows = 8 * NT;
     constexpr int kSteps = D / 16;  // k steps of Q K^T, and 16-row tiles of V^T
@@ -87,7 +133,13 @@ __global__ void __launch_bounds__(kThreads)
     const Tile t = tile_of(g, a, c.page, group, kRows, blockIdx.x);
     if (t.b < 0) return;
     const int splits = splits_of(t, chunk, gridDim.z);
-    if ((int)blockIdx.z >= splits) return;
+    if ((int)blockIdx.z >= splits) {
+        if (CLUSTER) {
+            cluster_sync();
+            cluster_sync();
+        }
+        return;
+    }
     const int begin = t.lo + (int)blockIdx.z * chunk;
     const int end = (int)blockIdx.z == splits - 1 ? t.hi : min(t.hi, begin + chunk);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
@@ -184,7 +236,18 @@ __global__ void __launch_bounds__(kThreads)
         }
         __syncthreads();
 
+        // A step's 16 tokens are contiguous in K and in V; they are asked into L2
+        // kAhead steps before the loads that wait for them.
+        auto ask = [&](int t0) {
+            if (t0 >= bend || lane > 1) return;
+            const int id = sm.id[(t0 >> shift) - p0];
+            if (id < 0) return;
+            const int64_t at = (((int64_t)id * c.heads + h) * c.page + (t0 & (c.page - 1))) * D;
+            prefetch_l2((lane ? c.v : c.k) + at, kStep * D);
+        };
+        for (int a0 = 0; a0 < kAhead; ++a0) ask(b0 + warp * kStep + a0 * kSplitTokens);
         for (int t0 = b0 + warp * kStep; t0 < bend; t0 += kSplitTokens) {
+            ask(t0 + kAhead * kSplitTokens);
             const int p = (t0 >> shift) - p0, id = sm.id[p];
             if (id < 0) continue;  // reported
             const int64_t block = ((int64_t)id * c.heads + h) * c.page + (t0 & (c.page - 1));
@@ -201,14 +264,15 @@ __global__ void __launch_bounds__(kThreads)
 
             float x[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.0f;
-#pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 const uint32_t a0 = codes_02(kw[0][s]), a1 = codes_02(kw[1][s]);
                 const uint32_t a2 = codes_02(kw[0][s] >> 8), a3 = codes_02(kw[1][s] >> 8);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    mma16816(x[n], a0, a1, a2, a3, qh[n][s][0], qh[n][s][1]);
+                    if (s == 0)
+                        mma16816_first(x[n], a0, a1, a2, a3, qh[n][s][0], qh[n][s][1]);
+                    else
+                        mma16816(x[n], a0, a1, a2, a3, qh[n][s][0], qh[n][s][1]);
                     mma16816(x[n], a0, a1, a2, a3, ql[n][s][0], ql[n][s][1]);
                 }
             }
@@ -270,11 +334,10 @@ __global__ void __launch_bounds__(kThreads)
                     // summed over the step by the tensor core, over the steps in
                     // rounded fp32: its own sums are cut off, which a long
                     // cache adds up (8192 tokens: 5e-6 against 1e-6)
-                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma16816(d, a0, a1, a2, a3, ph[n][0], ph[n][1]);
+                    float d[4];
+                    mma16816_first(d, a0, a1, a2, a3, ph[n][0], ph[n][1]);
                     mma16816(d, a0, a1, a2, a3, pl[n][0], pl[n][1]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[n][s][i] += d[i];
+                    add_pairs(o[n][s], d);
                 }
             }
         }
@@ -301,28 +364,20 @@ __global__ void __launch_bounds__(kThreads)
                 *reinterpret_cast<float2 *>(&sm.o[warp][row][(D / 8) * lg + 2 * s]) = make_float2(o[n][s][r], o[n][s][r + 2]);
         }
     __syncthreads();
+    const bool cluster = CLUSTER;
     for (int i = threadIdx.x; i < t.rows * (D / 4); i += kThreads) {
         const int r = i / (D / 4), d = 4 * (i - r * (D / 4));
-        float mm = sm.ml[0][0][r];
+        float mm = sm.ml[0][0][r], ll = sm.ml[1][0][r];
+        float4 v = *reinterpret_cast<const float4 *>(&sm.o[0][r][d]);
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, sm.ml[0][w][r]);
-        float ll = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float mw = sm.ml[0][w][r], f = mw == -inf ? 0.0f : ex2(mw - mm);
-            // a warp without a reference holds zeros, or the NaN of a poisoned page
-            const float4 x = *reinterpret_cast<const float4 *>(&sm.o[w][r][d]);
-            const float lw = sm.ml[1][w][r];
-            ll = fmaf(f, lw, ll);
-            v.x = fmaf(f, x.x, v.x);
-            v.y = fmaf(f, x.y, v.y);
-            v.z = fmaf(f, x.z, v.z);
-            v.w = fmaf(f, x.w, v.w);
-        }
+        for (int w = 1; w < kWarps; ++w)
+            join_part(mm, ll, v, sm.ml[0][w][r], sm.ml[1][w][r], *reinterpret_cast<const float4 *>(&sm.o[w][r][d]));
         const int row = t.s.row0 + (t.r0 + r) / group, head = h * group + (t.r0 + r) % group;
         const int64_t at = (int64_t)row * a.q_heads + head;
-        if (splits == 1) {
+        if (cluster) {  // for the other CTAs of the row
+            if (d == 0) sm.all[r] = make_float2(mm, ll);
+            *reinterpret_cast<float4 *>(&sm.o[0][r][d]) = v;
+        } else if (splits == 1) {
             if (d == 0) write_lse(a, at, mm, ll);
             write_out(a, at * D + d, v, ll);
         } else {
@@ -331,11 +386,35 @@ __global__ void __launch_bounds__(kThreads)
             *reinterpret_cast<float4 *>(to + 4 + d) = v;
         }
     }
+    if (!cluster) return;
+    // the splits' parts through the cluster's shared memory: CTA z joins each
+    // splits-th item
+    cluster_sync();
+    for (int i = threadIdx.x + (int)blockIdx.z * kThreads; i < t.rows * (D / 4); i += splits * kThreads) {
+        const int r = i / (D / 4), d = 4 * (i - r * (D / 4));
+        float m = -inf, l = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int z = 0; z < splits; ++z) {
+            const float4 ml = peer_load(smem_u32(&sm.all[r & ~1]), z);  // two rows' references and sums
+            join_part(m, l, v, r & 1 ? ml.z : ml.x, r & 1 ? ml.w : ml.y, peer_load(smem_u32(&sm.o[0][r][d]), z));
+        }
+        const int row = t.s.row0 + (t.r0 + r) / group, head = h * group + (t.r0 + r) % group;
+        const int64_t at = (int64_t)row * a.q_heads + head;
+        if (d == 0) write_lse(a, at, m, l);
+        write_out(a, at * D + d, v, l);
+    }
+    cluster_sync();  // nobody leaves while its memory is read
 }
 
-// Joins the splits of a unit's rows; grid: (units, cached heads).
-__global__ void __launch_bounds__(kThreads)
-    kv_attention_join_kernel(const Cache c, const Batch g, const Attend a, int tile_rows, int chunk, int splits, const float *part) {
+// Joins the splits of a unit's rows; grid: (units, cached heads, rows / rows
+// of a CTA). `sharing` groups of D / 4 threads take a row's parts in turn, each
+// thread four of its elements, and meet in shared memory.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads)
+    kv_attention_join_kernel(const Cache c, const Batch g, const Attend a, int tile_rows, int chunk, int splits, int sharing,
+                             const float *part) {
+    __shared__ float4 held[kJoinThreads];
+    __shared__ float2 held_ml[kJoinThreads];
     pdl_launch_dependents();
     pdl_wait();
     const int h = blockIdx.y, group = a.q_heads / c.heads, D = c.dim;
@@ -343,36 +422,47 @@ __global__ void __launch_bounds__(kThreads)
     if (t.b < 0) return;
     const int n = splits_of(t, chunk, splits);
     if (n == 1) return;
-    const float inf = __int_as_float(0x7F800000);
-    const int64_t step = (int64_t)tile_rows * (D + 4);
-    for (int i = threadIdx.x; i < t.rows * (D / 4); i += kThreads) {
-        const int r = i / (D / 4), d = 4 * (i - r * (D / 4));
+    const int width = D / 4, lane = threadIdx.x % width, who = threadIdx.x / width;
+    const int rows = kJoinThreads / width / sharing, share = who % sharing, r = blockIdx.z * rows + who / sharing, d = 4 * lane;
+    const bool in = who < rows * sharing && r < t.rows;
+    float m = -__int_as_float(0x7F800000), l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (in) {
+        const int64_t step = (int64_t)tile_rows * (D + 4);
         const float *p = part + (((int64_t)blockIdx.x * c.heads + h) * splits * tile_rows + r) * (D + 4);
-        float m = -inf;
-        for (int z = 0; z < n; ++z) m = fmaxf(m, p[z * step]);
-        float l = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int z = 0; z < n; ++z) {
+#pragma unroll 4
+        for (int z = share; z < n; z += sharing) {
             const float2 ml = *reinterpret_cast<const float2 *>(p + z * step);
-            const float4 x = *reinterpret_cast<const float4 *>(p + z * step + 4 + d);
-            const float f = ml.x == -inf ? 0.0f : ex2(ml.x - m);
-            l = fmaf(f, ml.y, l);
-            v.x = fmaf(f, x.x, v.x);
-            v.y = fmaf(f, x.y, v.y);
-            v.z = fmaf(f, x.z, v.z);
-            v.w = fmaf(f, x.w, v.w);
+            join_part(m, l, o, ml.x, ml.y, *reinterpret_cast<const float4 *>(p + z * step + 4 + d));
         }
-        const int row = t.s.row0 + (t.r0 + r) / group, head = h * group + (t.r0 + r) % group;
-        const int64_t at = (int64_t)row * a.q_heads + head;
-        if (d == 0) write_lse(a, at, m, l);
-        write_out(a, at * D + d, v, l);
     }
+    held[threadIdx.x] = o;
+    held_ml[threadIdx.x] = make_float2(m, l);
+    __syncthreads();
+    if (!in || share != 0) return;
+    for (int k = 1; k < sharing; ++k) {
+        const float2 ml = held_ml[threadIdx.x + k * width];
+        join_part(m, l, o, ml.x, ml.y, held[threadIdx.x + k * width]);
+    }
+    const int row = t.s.row0 + (t.r0 + r) / group, head = h * group + (t.r0 + r) % group;
+    const int64_t at = (int64_t)row * a.q_heads + head;
+    if (d == 0) write_lse(a, at, m, l);
+    write_out(a, at * D + d, o, l);
 }
 
 // Tokens that the tensor cores may sum for an fp32 output.
 constexpr int64_t kSumTokens = 1024;
 // Rows of a sequence up to which a tile is eight or sixteen of them.
 constexpr int64_t kFewRows = 64;
+// Splits of few rows join in a (portable) cluster where all CTAs run at once:
+// no second launch and no workspace. In more than one wave the members of a
+// cluster would wait for one another (64 sequences of up to 8192 tokens: 202
+// us, 149 with a second kernel).
+constexpr int kClusterMax = 8;
+constexpr int64_t kClusterTokens = 4096;  // up to which more splits are not worth a second launch
+bool joins_in_cluster(const Plan &p, int64_t tiles) {
+    return p.tile_rows != kPrefillRows && p.splits > 1 && p.splits <= kClusterMax && tiles * p.splits <= 4 * kSms;
+}
 Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv, int64_t window,
              int ft) {
     Plan p;
@@ -386,27 +476,36 @@ Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_
     const int64_t tiles = (T * group + p.tile_rows - 1) / p.tile_rows;  // about as many have rows
     int64_t kv = max_kv < 1 ? 1 : max_kv;
     if (window && window + max_q < kv) kv = window + max_q;
-    // Enough CTAs for every SM to hold several, and for ragged lengths to even out.
-    const int64_t want = 8 * kSms / (tiles * heads > 0 ? tiles * heads : 1);
+    // CTAs for every SM to hold four and two waves of them; where there are many
+    // anyway (ragged lengths), four waves, so that they even out.
+    const int64_t ctas = tiles * heads > 0 ? tiles * heads : 1;
+    const int64_t want = (ctas < kSms || p.tile_rows == kPrefillRows ? 8 : 16) * kSms / ctas;
     int64_t splits = want < 1 ? 1 : want;
     const int64_t most = (kv + kSplitTokens - 1) / kSplitTokens;
     if (splits > most) splits = most;
+    // a short cache is read sooner than a second kernel starts
+    if (p.tile_rows != kPrefillRows && kv <= kClusterTokens && splits > kClusterMax) splits = kClusterMax;
     if (splits > 256) splits = 256;
     if (p.tile_rows == kPrefillRows && ft == QMM_F32 && splits < (kv + kSumTokens - 1) / kSumTokens) splits = (kv + kSumTokens - 1) / kSumTokens;
     p.chunk = (int)(((kv + splits - 1) / splits + kSplitTokens - 1) / kSplitTokens * kSplitTokens);
     p.splits = (int)((kv + p.chunk - 1) / p.chunk);
+    p.cluster = joins_in_cluster(p, ctas);
     return p;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool CLUSTER>
 cudaError_t launch_tiles(const Cache &c, const Batch &g, const Rope &r, const Attend &a, const Plan &p, float *part, cudaStream_t s) {
     static std::atomic<uint64_t> ready{0};  // devices whose shared memory limit is set
-    auto kernel = kv_attention_kernel<D, NT>;
+    auto kernel = kv_attention_kernel<D, NT, CLUSTER>;
     constexpr int smem = (int)sizeof(Smem<D, NT>);
     const cudaError_t es = allow_smem((const void *)kernel, smem, ready);
     if (es != cudaSuccess) return es;
     const dim3 grid((unsigned)p.units, (unsigned)c.heads, (unsigned)p.splits);
-    return launch(kernel, grid, kThreads, smem, s, c, g, r, a, p.chunk, part);
+    return launch_clusters(kernel, grid, kThreads, smem, CLUSTER ? p.splits : 1, s, c, g, r, a, p.chunk, part);
+}
+template <int D, int NT>
+cudaError_t launch_tiles(const Cache &c, const Batch &g, const Rope &r, const Attend &a, const Plan &p, float *part, cudaStream_t s) {
+    return p.cluster ? launch_tiles<D, NT, true>(c, g, r, a, p, part, s) : launch_tiles<D, NT, false>(c, g, r, a, p, part, s);
 }
 
 }  // namespace
@@ -415,7 +514,7 @@ size_t kv_attention_bytes(int heads, int dim, int page, int batch, int q_heads, 
     (void)page;
     // for any window: a window only lowers the number of splits' tokens, not their bound
     const Plan p = plan_of(heads, dim, batch, q_heads, T, max_q, max_kv, 0, QMM_F32);
-    return p.splits == 1 ? 0 : (size_t)p.units * heads * p.splits * p.tile_rows * (dim + 4) * 4;
+    return p.splits == 1 || p.cluster ? 0 : (size_t)p.units * heads * p.splits * p.tile_rows * (dim + 4) * 4;
 }
 
 cudaError_t launch_kv_attention(const Cache &c, const Batch &g, const Rope &r, const Attend &a, void *ws, cudaStream_t s) {
@@ -432,9 +531,13 @@ cudaError_t launch_kv_attention(const Cache &c, const Batch &g, const Rope &r, c
     case 192: e = launch_tiles<192, 1>(c, g, r, a, p, part, s); break;
     default: e = launch_tiles<256, 1>(c, g, r, a, p, part, s); break;
     }
-    if (e != cudaSuccess || p.splits == 1) return e;
-    return launch(kv_attention_join_kernel, dim3((unsigned)p.units, (unsigned)c.heads), kThreads, 0, s, c, g, a, p.tile_rows,
-                  p.chunk, p.splits, (const float *)part);
+    if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
+    // a group of threads for each row, more for each eight splits
+    const int groups = kJoinThreads / (c.dim / 4), most = p.splits / 8 < groups ? p.splits / 8 : groups;
+    const int sharing = p.tile_rows == kPrefillRows || most < 1 ? 1 : most, rows = groups / sharing;
+    const dim3 grid((unsigned)p.units, (unsigned)c.heads, (unsigned)((p.tile_rows + rows - 1) / rows));
+    return launch(kv_attention_join_kernel, grid, kJoinThreads, 0, s, c, g, a, p.tile_rows, p.chunk, p.splits, sharing,
+                  (const float *)part);
 }
 
 }  // namespace serving

@@ -84,11 +84,12 @@ __device__ __forceinline__ void write_out(const Attend &a, int64_t at, float4 o,
 }
 
 // How a call is split: rows of a tile, upper bound of tiles, tokens and
-// number of splits.
+// number of splits, and whether the splits join in a cluster.
 struct Plan {
     int tile_rows;
     int64_t units;
     int chunk, splits;
+    bool cluster;
 };
 constexpr int kSplitTokens = 64;  // splits begin at multiples of this
 constexpr int kPrefillRows = 128;

@@ -175,20 +175,28 @@ __device__ __forceinline__ void rotate_item(const Rope &r, int j, int64_t pos, f
 // Every serving kernel is launched so that it may start while its predecessor
 // ends, and waits for that one's results first (pdl_wait).
 template <class... P, class... A>
-inline cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+inline cudaError_t launch_clusters(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster_z, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = (unsigned)cluster_z;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster_z > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
     count_launch();
     return e;
+}
+template <class... P, class... A>
+inline cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    return launch_clusters(kernel, grid, threads, smem, 1, s, args...);
 }
 
 // Lets `kernel` use `bytes` of shared memory on the current device, once per
