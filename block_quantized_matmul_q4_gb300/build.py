@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libqmm.so")
 
 SOURCES = ["api.cu", "quantize.cu", "repack.cu", "gemv.cu", "debug.cu", "static_scratch.cu", "tmap.cu",
            "w4a16.cu", "gemm_f16.cu", "gemv_mma.cu", "gemv_mma6.cu", "streamk.cu", "peaks.cu",
-           "serving_api.cu", "kv_cache.cu", "kv_attention.cu", "kv_prefill.cu", "logprobs.cu"]
+           "serving_api.cu", "kv_cache.cu", "kv_attention.cu", "kv_prefill.cu", "kv_prefill_wide.cu",
+           "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
                  "-I", CSRC, "--expt-relaxed-constexpr"]

@@ -450,8 +450,8 @@ __global__ void __launch_bounds__(kJoinThreads)
     write_out(a, at * D + d, o, l);
 }
 
-// Tokens that the tensor cores may sum for an fp32 output.
-constexpr int64_t kSumTokens = 1024;
+// Tokens that kv_prefill_wide.cu's tensor cores may sum for an fp32 output.
+constexpr int64_t kSumTokens = 512;
 // Rows of a sequence up to which a tile is eight or sixteen of them.
 constexpr int64_t kFewRows = 64;
 // Splits of few rows join in a (portable) cluster where all CTAs run at once:
@@ -486,7 +486,7 @@ Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_
     // a short cache is read sooner than a second kernel starts
     if (p.tile_rows != kPrefillRows && kv <= kClusterTokens && splits > kClusterMax) splits = kClusterMax;
     if (splits > 256) splits = 256;
-    if (p.tile_rows == kPrefillRows && ft == QMM_F32 && splits < (kv + kSumTokens - 1) / kSumTokens) splits = (kv + kSumTokens - 1) / kSumTokens;
+    if (p.tile_rows == kPrefillRows && dim > 128 && ft == QMM_F32 && splits < (kv + kSumTokens - 1) / kSumTokens) splits = (kv + kSumTokens - 1) / kSumTokens;
     p.chunk = (int)(((kv + splits - 1) / splits + kSplitTokens - 1) / kSplitTokens * kSplitTokens);
     p.splits = (int)((kv + p.chunk - 1) / p.chunk);
     p.cluster = joins_in_cluster(p, ctas);

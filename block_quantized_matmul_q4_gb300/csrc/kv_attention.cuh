@@ -72,8 +72,7 @@ __device__ __forceinline__ int splits_of(const Tile &t, int chunk, int splits) {
 __device__ __forceinline__ void write_lse(const Attend &a, int64_t at, float m, float l) {
     if (a.lse) a.lse[at] = l == 0.0f ? __int_as_float(0xFF800000) : (m + log2f(l)) * 0.693147180559945f;
 }
-__device__ __forceinline__ void write_out(const Attend &a, int64_t at, float4 o, float l) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+__device__ __forceinline__ void write_scaled(const Attend &a, int64_t at, float4 o, float inv) {
     o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     if (a.ft == QMM_F32)
         store4<QMM_F32>(a.out, at, o);
@@ -81,6 +80,10 @@ __device__ __forceinline__ void write_out(const Attend &a, int64_t at, float4 o,
         store4<QMM_F16>(a.out, at, o);
     else
         store4<QMM_BF16>(a.out, at, o);
+}
+
+__device__ __forceinline__ void write_out(const Attend &a, int64_t at, float4 o, float l) {
+    write_scaled(a, at, o, l == 0.0f ? 0.0f : 1.0f / l);
 }
 
 // How a call is split: rows of a tile, upper bound of tiles, tokens and

@@ -1,153 +1,87 @@
 // kv_prefill.cu -- attention over the paged 8-bit cache for many rows per
-// sequence, on the tcgen05 tensor cores. The mathematics is kv_attention.cu's.
+// sequence, on the tcgen05 tensor cores, for head_dim up to 128. The
+// mathematics is kv_attention.cu's.
 //
 // A CTA takes 128 rows (new tokens x the query heads that share a cached
-// head), one per TMEM lane, and walks the tokens they see 64 at a time:
-//   S = Q K^T   128 x 64, both operands in shared memory (128-byte swizzle);
-//   P           four warps, a thread per row: S from TMEM, weights, back into
-//               the same TMEM columns as fp16 (or two of them);
-//   O += P V    128 x head_dim, P from TMEM, V^T in shared memory.
-// Four more warps turn the codes into the fp16 operands (K as it lies, V
-// transposed, both exact) while the softmax runs, one thread issues the MMAs.
-// S has two TMEM buffers, so the next tile's scores are taken while this
-// one's weights are computed; two CTAs share an SM (head_dim up to 128), so
-// that the tensor cores work for one while the other waits for its softmax.
+// head), one per TMEM lane, and walks the tokens they see 64 at a time, as a
+// pipeline of warps:
+//   producer     a tile's codes from its pages into a ring of four stages
+//                (bulk copies: whole rows of a page are contiguous);
+//   converters   codes to the fp16 operands (exact): K as it lies, V
+//                transposed, in the 128-byte swizzle, two buffers each;
+//   MMA issuer   S = Q K^T (128 x 64) into one of two TMEM buffers; O += P V
+//                (128 x head_dim), P from TMEM;
+//   softmax      eight warps, two threads a row: S from TMEM, weights, back
+//                into the same columns as one or two fp16 numbers;
+//   joiners      four warps, a thread a row, see below.
+// The next tile's scores are taken while this one's weights are computed, so
+// the tensor cores are what bounds it (2 x head_dim x 64 x 128 products a
+// tile, twice each where Q and P are two numbers).
 //
-// O stays in TMEM; a row whose reference is renewed (a weight would pass
-// 2^15) has it multiplied there, which is rare. The tensor cores cut their
-// sums off rather than round them, which 8192 tokens add up to 1.7e-5 of the
-// result: for fp32 outputs a call is split so that no O sums more than 1024.
-#include "kv_attention.cuh"
-#include "tc.cuh"
+// The tensor cores cut their sums off rather than round them: over 8192 tokens
+// in one accumulator, 1.7e-5 of the result. So the tiles come in blocks of
+// kBlock with an O of their own (two TMEM buffers in turn), relative to a
+// reference of their own, which the joiners add to the whole O (in TMEM too)
+// in rounded fp32 while the next block runs. A weight that would pass 2^15
+// begins a new block with a new reference early, so nothing is ever rescaled
+// in the middle.
+#include "kv_prefill.cuh"
 
 namespace qmm {
 namespace serving {
 namespace {
 
-constexpr int kRows = kPrefillRows, kTok = 64;  // rows of a CTA, tokens of a tile
-constexpr int kSoftWarps = 4, kConvWarps = 4;
-constexpr int kConv = kConvWarps * 32;
-constexpr int kMmaWarp = kSoftWarps + kConvWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
-static_assert(kSoftWarps * 32 == kRows && kTok == kSplitTokens, "a thread for each row, splits at tiles");
+constexpr int kRows = kPrefillRows;
+constexpr int kSoftWarps = 8, kConvWarps = 4, kJoinWarps = 4;
+constexpr int kConvWarp0 = kSoftWarps, kJoinWarp0 = kConvWarp0 + kConvWarps, kMmaWarp = kJoinWarp0 + kJoinWarps,
+              kLoadWarp = kMmaWarp + 1;
+constexpr int kSoft = kSoftWarps * 32, kConv = kConvWarps * 32, kJoin = kJoinWarps * 32;
+constexpr int kThreads = (kLoadWarp + 1) * 32;
+constexpr int kStages = 4;  // tiles of codes on their way
+constexpr int kBlock = 8;   // tiles that share an O: their cut-off stays below 1e-6
+constexpr int kHalf = kTok / 2;
+static_assert(kSoft == 2 * kRows && kJoin == kRows, "threads of a row");
 
-// Shared memory: Q (one or two parts), K, V^T, then the rest.
+struct Tail {  // behind the operands
+    uint64_t raw_full[kStages], raw_empty[kStages], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], block_full[2],
+        block_empty[2], pv_done, done;
+    uint32_t tmem;
+    int begins[2];             // tile i (slot i & 1) begins a block
+    int last[2];               // block b (slot b & 1) is the last one
+    float most[2][2][kRows];   // [tile & 1][half]: a row's largest score
+    float m[4][kRows], l[4][2][kRows];  // [block & 3]: reference and sums of a row
+    float down[kRows];         // what undoes the power of two of each row of Q
+};
+
 template <int D>
 struct Shape {
     static constexpr int kChunks = (D + 63) / 64;  // 64-element slices of a head, 128 bytes a row
     static constexpr int kQBytes = kChunks * kRows * 128, kKBytes = kChunks * kTok * 128, kVBytes = D * 128;
-    static constexpr int kTmemO = 2 * kTok;  // S and P buffers, then O
-    static constexpr int kTmemCols = kTmemO + D <= 256 ? 256 : 512;
-    static constexpr int kCtas = kTmemCols == 256 ? 2 : 1;
-    static constexpr int bytes(int q_parts) { return q_parts * kQBytes + kKBytes + kVBytes + 1024; }
-    static_assert(bytes(2) <= (kCtas == 2 ? 113 : 227) * 1024, "shared memory");
+    static constexpr int kRaw = kTok * D;  // codes of K, or of V, of a tile
+    static constexpr int kBlockCol = 2 * kTok, kWholeCol = kBlockCol + 2 * D;  // TMEM: S and P, O of two blocks, the whole O
+    static_assert(kWholeCol + D <= 512, "TMEM");
+    static constexpr int bytes(int q_parts) { return q_parts * kQBytes + 2 * (kKBytes + kVBytes) + kStages * 2 * kRaw + (int)sizeof(Tail); }
 };
 
-struct Tail {  // behind the operands
-    uint64_t k_full, k_empty, v_full, pv_done, s_full[2], p_full[2], done;
-    uint32_t tmem;
-    float down[kRows];  // what undoes the power of two of each row of Q
-};
-static_assert(sizeof(Tail) <= 1024, "tail");
-
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-// Waits for the thread's TMEM loads. Their results pass through, so that no
-// use of them is scheduled before the wait.
-__device__ __forceinline__ void ld_wait16(float (&v)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
-                   "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
-                 :
+// Whether any of the softmax threads says yes; a barrier among them.
+__device__ __forceinline__ bool any_of_soft(bool yes) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.or.pred p, 3, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)yes), "n"(kSoft)
                  : "memory");
-}
-__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// The row's elements as fp16 (one or two parts), each quad stored as (0, 2,
-// 1, 3): the order in which codes_02 gives a word's codes. Two threads a row.
-template <int D>
-__device__ __forceinline__ void load_q(const Batch &g, const Rope &rope, const Attend &a, const Cache &c, const Tile &t, int h, int group,
-                                       int q_parts, uint8_t *smem, Tail *tail) {
-    using S = Shape<D>;
-    const int r = threadIdx.x >> 1, half = threadIdx.x & 1;
-    const int row = (t.r0 + r) / group, head = h * group + (t.r0 + r) % group;
-    const int64_t at = (int64_t)(t.s.row0 + row) * a.Q.stride + (int64_t)head * D;
-    auto item = [&](int j, float4 &x, float4 &y) {
-        const int2 q = quad_at(rope, j);
-        x = y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (r < t.rows) {
-            if (a.ft == QMM_F32) {
-                x = load4<QMM_F32>(a.Q.p, at + q.x), y = load4<QMM_F32>(a.Q.p, at + q.y);
-            } else if (a.ft == QMM_F16) {
-                x = load4<QMM_F16>(a.Q.p, at + q.x), y = load4<QMM_F16>(a.Q.p, at + q.y);
-            } else {
-                x = load4<QMM_BF16>(a.Q.p, at + q.x), y = load4<QMM_BF16>(a.Q.p, at + q.y);
-            }
-            rotate_item(rope, j, t.start + row, x, y);
-        }
-        return q;
-    };
-    uint32_t most = 0;
-    for (int j = half; j < D / 8; j += 2) {
-        float4 x, y;
-        item(j, x, y);
-        most = max(max(most, __float_as_uint(x.x) & 0x7FFFFFFFu), __float_as_uint(x.y) & 0x7FFFFFFFu);
-        most = max(max(most, __float_as_uint(x.z) & 0x7FFFFFFFu), __float_as_uint(x.w) & 0x7FFFFFFFu);
-        most = max(max(most, __float_as_uint(y.x) & 0x7FFFFFFFu), __float_as_uint(y.y) & 0x7FFFFFFFu);
-        most = max(max(most, __float_as_uint(y.z) & 0x7FFFFFFFu), __float_as_uint(y.w) & 0x7FFFFFFFu);
-    }
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    const float2 f = row_scale(most);
-    if (half == 0) tail->down[r] = f.y;
-    auto store = [&](int d, float4 v) {
-        v = make_float4(v.x * f.x, v.y * f.x, v.z * f.x, v.w * f.x);
-        uint8_t *to = smem + (d >> 6) * (kRows * 128) + r * 128 + ((((d & 63) >> 3) ^ (r & 7)) << 4) + (d & 4) * 2;
-        const uint32_t h0 = half_pair(v.x, v.z), h1 = half_pair(v.y, v.w);
-        *reinterpret_cast<uint2 *>(to) = make_uint2(h0, h1);
-        if (q_parts == 2) *reinterpret_cast<uint2 *>(to + S::kQBytes) = make_uint2(rest_pair(v.x, v.z, h0), rest_pair(v.y, v.w, h1));
-    };
-    for (int j = half; j < D / 8; j += 2) {
-        float4 x, y;
-        const int2 q = item(j, x, y);
-        store(q.x, x);
-        store(q.y, y);
-    }
+    return r != 0;
 }
 
 // PARTS: fp16 numbers that a weight is given as.
 template <int D, int PARTS>
-__global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
+__global__ void __launch_bounds__(kThreads, 1)
     kv_prefill_kernel(const Cache c, const Batch g, const Rope rope, const Attend a, int chunk, int q_parts, float *part) {
     using S = Shape<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
-    Tail *tail = reinterpret_cast<Tail *>(smem + q_parts * S::kQBytes + S::kKBytes + S::kVBytes);
-    const uint32_t q_at = base, k_at = base + q_parts * S::kQBytes, v_at = k_at + S::kKBytes;
+    const uint32_t q_at = base, k_at = q_at + q_parts * S::kQBytes, v_at = k_at + 2 * S::kKBytes, raw_at = v_at + 2 * S::kVBytes;
+    Tail *tail = reinterpret_cast<Tail *>(smem + (raw_at - base) + kStages * 2 * S::kRaw);
     pdl_launch_dependents();
     pdl_wait();
     const int h = blockIdx.y, group = a.q_heads / c.heads;
@@ -161,29 +95,72 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
     const int tiles = (end - begin + kTok - 1) / kTok;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int shift = 31 - __clz(c.page);
+    const int32_t *ids = g.table + (int64_t)t.b * g.max_pages;
+    const float inf = __int_as_float(0x7F800000);
 
     if (threadIdx.x == 0) {
-        mbar_init(smem_u32(&tail->k_full), kConv);
-        mbar_init(smem_u32(&tail->v_full), kConv);
-        mbar_init(smem_u32(&tail->k_empty), 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&tail->raw_full[i]), 1);
+            mbar_init(smem_u32(&tail->raw_empty[i]), kConv);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&tail->k_full[i]), kConv);
+            mbar_init(smem_u32(&tail->k_empty[i]), 1);
+            mbar_init(smem_u32(&tail->v_full[i]), kConv);
+            mbar_init(smem_u32(&tail->v_empty[i]), 1);
+            mbar_init(smem_u32(&tail->s_full[i]), 1);
+            mbar_init(smem_u32(&tail->p_full[i]), kSoft);
+            mbar_init(smem_u32(&tail->block_full[i]), 2);  // its MMAs, and the issuer's word that `last` is written
+            mbar_init(smem_u32(&tail->block_empty[i]), kJoin);
+        }
         mbar_init(smem_u32(&tail->pv_done), 1);
         mbar_init(smem_u32(&tail->done), 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&tail->s_full[i]), 1);
-            mbar_init(smem_u32(&tail->p_full[i]), kRows);
-        }
         fence_barrier_init();
     }
     __syncwarp();
-    if (warp == kMmaWarp) tc::tmem_alloc(smem_u32(&tail->tmem), S::kTmemCols);
-    if (warp < kMmaWarp) load_q<D>(g, rope, a, c, t, h, group, q_parts, smem, tail);
+    if (warp == kMmaWarp) tc::tmem_alloc(smem_u32(&tail->tmem), 512);
+    if (warp < kSoftWarps) load_q<D>(g, rope, a, c, t, h, group, q_parts, smem, tail->down);
     tc::fence_proxy_async();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = tail->tmem;
 
-    if (warp == kMmaWarp) {
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            const uint64_t policy = policy_evict_last();  // the other rows' CTAs read the same pages
+            int issued = 0;
+            for (int i = 0; i < tiles; ++i) {
+                const int s = i % kStages;
+                if (i >= kStages && !mbar_wait(smem_u32(&tail->raw_empty[s]), (uint32_t)((i / kStages - 1) & 1), g.err)) break;
+                // the tile's pieces of pages; tokens past the end stay what they were (masked)
+                const int t0 = begin + i * kTok, t1 = min(t0 + kTok, end);
+                uint32_t bytes = 0;
+                for (int token = t0; token < t1; token = ((token >> shift) + 1) << shift) {
+                    const int id = ids[token >> shift], n = min((((token >> shift) + 1) << shift), t0 + kTok) - token;
+                    if (id >= 0 && id < g.num_pages)
+                        bytes += 2 * n * D;
+                    else
+                        atomicOr(g.err, kDevErrRange);
+                }
+                const uint32_t bar = smem_u32(&tail->raw_full[s]), to = raw_at + s * 2 * S::kRaw;
+                mbar_arrive_expect_tx(bar, bytes);
+                for (int token = t0; token < t1; token = ((token >> shift) + 1) << shift) {
+                    const int id = ids[token >> shift], n = min((((token >> shift) + 1) << shift), t0 + kTok) - token;
+                    if (id < 0 || id >= g.num_pages) continue;
+                    const int64_t from = (((int64_t)id * c.heads + h) * c.page + (token & (c.page - 1))) * D;
+                    bulk_g2s(to + (token - t0) * D, c.k + from, n * D, bar, policy);
+                    bulk_g2s(to + S::kRaw + (token - t0) * D, c.v + from, n * D, bar, policy);
+                }
+                ++issued;
+            }
+            // copies in flight land before the CTA ends
+            for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+                mbar_wait(smem_u32(&tail->raw_full[i % kStages]), (uint32_t)((i / kStages) & 1), g.err);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
             constexpr uint32_t idesc_s = tc::idesc_f16_f32(kRows, kTok), idesc_o = tc::idesc_f16_f32(kRows, D);
@@ -192,166 +169,158 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
             // have been used (MMAs of different shapes keep no order).
             auto scores = [&](int i) {
                 if (i > 1 && !mbar_wait(smem_u32(&tail->pv_done), (uint32_t)(i & 1), g.err)) return false;
-                if (!mbar_wait(smem_u32(&tail->k_full), (uint32_t)(i & 1), g.err)) return false;
+                if (!mbar_wait(smem_u32(&tail->k_full[i & 1]), (uint32_t)((i >> 1) & 1), g.err)) return false;
                 tc::fence_after_sync();
+                const uint64_t kb = kd + (((i & 1) * S::kKBytes) >> 4);
                 for (int p = 0; p < q_parts; ++p)
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         tc::mma_f16(tmem + (i & 1) * kTok, qd + ((p * S::kQBytes + (k >> 2) * (kRows * 128)) >> 4) + 2 * (k & 3),
-                                    kd + (((k >> 2) * (kTok * 128)) >> 4) + 2 * (k & 3), idesc_s, (p | k) != 0);
-                tc::commit(smem_u32(&tail->k_empty));
+                                    kb + (((k >> 2) * (kTok * 128)) >> 4) + 2 * (k & 3), idesc_s, (p | k) != 0);
+                tc::commit(smem_u32(&tail->k_empty[i & 1]));
                 tc::commit(smem_u32(&tail->s_full[i & 1]));
                 return true;
+            };
+            int block = -1;
+            auto end_block = [&](bool last) {
+                tail->last[block & 1] = last;
+                tc::commit(smem_u32(&tail->block_full[block & 1]));
+                mbar_arrive(smem_u32(&tail->block_full[block & 1]));
             };
             bool ok = scores(0);
             for (int i = 0; i < tiles && ok; ++i) {
                 if (i + 1 < tiles) ok = scores(i + 1);
-                ok = ok && mbar_wait(smem_u32(&tail->v_full), (uint32_t)(i & 1), g.err) &&
+                ok = ok && mbar_wait(smem_u32(&tail->v_full[i & 1]), (uint32_t)((i >> 1) & 1), g.err) &&
                      mbar_wait(smem_u32(&tail->p_full[i & 1]), (uint32_t)((i >> 1) & 1), g.err);
                 if (!ok) break;
+                const bool begins = tail->begins[i & 1] != 0;
+                if (begins) {
+                    if (block >= 0) end_block(false);
+                    ++block;
+                    if (block > 1) ok = mbar_wait(smem_u32(&tail->block_empty[block & 1]), (uint32_t)(((block >> 1) & 1) ^ 1), g.err);
+                    if (!ok) break;
+                }
                 tc::fence_after_sync();
+                const uint64_t vb = vd + (((i & 1) * S::kVBytes) >> 4);
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p)
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k)
-                        tc::mma_f16_ta(tmem + S::kTmemO, tmem + (i & 1) * kTok + p * (kTok / 2) + 8 * k, vd + 2 * k, idesc_o,
-                                       (i | p | k) != 0);
+                        tc::mma_f16_ta(tmem + S::kBlockCol + (block & 1) * D, tmem + (i & 1) * kTok + p * kHalf + 8 * k, vb + 2 * k,
+                                       idesc_o, !begins || (p | k) != 0);
+                tc::commit(smem_u32(&tail->v_empty[i & 1]));
                 tc::commit(smem_u32(&tail->pv_done));
             }
+            if (ok) end_block(true);
             tc::commit(smem_u32(&tail->done));
             mbar_wait(smem_u32(&tail->done), 0, g.err);  // no MMA may run when TMEM is freed
         }
         __syncwarp();
-    } else if (warp >= kSoftWarps) {
-        // ------------------------------------------------------------ codes to operands
-        const int tid = threadIdx.x - kSoftWarps * 32;
-        constexpr int kKLoads = D / 32;                // 16 codes each: D / 16 a token, 64 tokens
-        constexpr int kVLoads = (D + kConv - 1) / kConv;  // 8 x 8 codes each: D / 8 times 8
-        const int32_t *ids = g.table + (int64_t)t.b * g.max_pages;
-        // codes of a token, null where there is none
-        auto codes = [&](const int8_t *p, int token) -> const int8_t * {
-            if (token >= end) return nullptr;
-            const int id = ids[token >> shift];
-            if (id < 0 || id >= g.num_pages) {
-                atomicOr(g.err, kDevErrRange);
-                return nullptr;
-            }
-            return p + (((int64_t)id * c.heads + h) * c.page + (token & (c.page - 1))) * D;
-        };
-        uint4 kr[kKLoads];
-        uint2 vr[kVLoads][8];
-        auto load_k = [&](int i) {
+    } else if (warp >= kJoinWarp0) {
+        // ------------------------------------------------------------ joiners
+        const int r = threadIdx.x - kJoinWarp0 * 32;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const int64_t at = (int64_t)(t.s.row0 + (t.r0 + r) / group) * a.q_heads + h * group + (t.r0 + r) % group;
+        float *const to_part = part + (((unit * c.heads + h) * gridDim.z + blockIdx.z) * kRows + r) * (D + 4);
+        float m = -inf, l = 0.0f;
+        for (int b = 0;; ++b) {
+            if (!mbar_wait_warp(smem_u32(&tail->block_full[b & 1]), (uint32_t)((b >> 1) & 1), g.err)) break;
+            __syncwarp();
+            tc::fence_after_sync();
+            const bool last = tail->last[b & 1] != 0;
+            const float bm = tail->m[b & 3][r], bl = tail->l[b & 3][0][r] + tail->l[b & 3][1][r];
+            const float n = fmaxf(m, bm), f = m == -inf ? 0.0f : ex2(m - n), e = bm == -inf ? 0.0f : ex2(bm - n);
+            m = n;
+            l = fmaf(e, bl, f * l);
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 16) {
+                float o[16], w[16];
+                tc::tmem_ld16(lanes + S::kBlockCol + (b & 1) * D + d, o);
+                if (b > 0) tc::tmem_ld16(lanes + S::kWholeCol + d, w);
+                ld_wait16(o);
+                if (b > 0) {
+                    ld_wait16(w);
 #pragma unroll
-            for (int n = 0; n < kKLoads; ++n) {
-                const int task = n * kConv + tid, token = task / (D / 16), seg = task % (D / 16);
-                const int8_t *p = codes(c.k, begin + i * kTok + token);
-                kr[n] = p ? ld128(p + 16 * seg) : make_uint4(0, 0, 0, 0);
-            }
-        };
-        auto store_k = [&]() {
-#pragma unroll
-            for (int n = 0; n < kKLoads; ++n) {
-                const int task = n * kConv + tid, token = task / (D / 16), seg = task % (D / 16);
-                const uint32_t w[4] = {kr[n].x, kr[n].y, kr[n].z, kr[n].w};
-                uint32_t o[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    o[2 * k] = codes_02(w[k]);
-                    o[2 * k + 1] = codes_02(w[k] >> 8);
-                }
-                const uint32_t to = k_at + (seg >> 2) * (kTok * 128) + token * 128;
-                const int c0 = 2 * (seg & 3), sw = token & 7;
-                // the upper half of a row's segments store their chunks the other way round: no bank twice
-                if (seg & 4) {
-                    sts128(to + (((c0 + 1) ^ sw) << 4), o[4], o[5], o[6], o[7]);
-                    sts128(to + ((c0 ^ sw) << 4), o[0], o[1], o[2], o[3]);
+                    for (int k = 0; k < 16; ++k) o[k] = fmaf(e, o[k], f * w[k]);
                 } else {
-                    sts128(to + ((c0 ^ sw) << 4), o[0], o[1], o[2], o[3]);
-                    sts128(to + (((c0 + 1) ^ sw) << 4), o[4], o[5], o[6], o[7]);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] *= e;
                 }
-            }
-        };
-        auto load_v = [&](int i) {
+                if (!last) {
+                    tc::tmem_st16(lanes + S::kWholeCol + d, *reinterpret_cast<uint32_t(*)[16]>(&o));
+                } else if (r < t.rows) {
 #pragma unroll
-            for (int n = 0; n < kVLoads; ++n) {
-                const int task = n * kConv + tid, tg = task & 7, dg = task >> 3;
-                // eight tokens from a multiple of eight on: one page
-                const int token = begin + i * kTok + 8 * tg;
-                const int8_t *p = dg < D / 8 ? codes(c.v, token) : nullptr;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) vr[n][k] = p && token + k < end ? ld64(p + k * D + 8 * dg) : make_uint2(0, 0);
-            }
-        };
-        auto store_v = [&]() {
-#pragma unroll
-            for (int n = 0; n < kVLoads; ++n) {
-                const int task = n * kConv + tid, tg = task & 7, dg = task >> 3;
-                if (dg >= D / 8) continue;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    // y[q][b]: byte b of the word (dim 4 half + b) of tokens 4q .. 4q + 3 in the order 0, 2, 1, 3
-                    uint32_t y[2][4];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint32_t w0 = half ? vr[n][4 * q].y : vr[n][4 * q].x, w1 = half ? vr[n][4 * q + 1].y : vr[n][4 * q + 1].x;
-                        const uint32_t w2 = half ? vr[n][4 * q + 2].y : vr[n][4 * q + 2].x, w3 = half ? vr[n][4 * q + 3].y : vr[n][4 * q + 3].x;
-                        const uint32_t lo01 = __byte_perm(w0, w1, 0x5140), hi01 = __byte_perm(w0, w1, 0x7362);
-                        const uint32_t lo23 = __byte_perm(w2, w3, 0x5140), hi23 = __byte_perm(w2, w3, 0x7362);
-                        y[q][0] = __byte_perm(lo01, lo23, 0x5140);
-                        y[q][1] = __byte_perm(lo01, lo23, 0x7362);
-                        y[q][2] = __byte_perm(hi01, hi23, 0x5140);
-                        y[q][3] = __byte_perm(hi01, hi23, 0x7362);
-                    }
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const int d = 8 * dg + 4 * half + b;
-                        sts128(v_at + d * 128 + ((tg ^ (d & 7)) << 4), codes_02(y[0][b]), codes_02(y[0][b] >> 8), codes_02(y[1][b]),
-                               codes_02(y[1][b] >> 8));
+                    for (int k = 0; k < 16; k += 4) {
+                        const float4 v = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        if (splits == 1)
+                            write_scaled(a, at * D + d + k, v, inv);
+                        else
+                            *reinterpret_cast<float4 *>(to_part + 4 + d + k) = v;
                     }
                 }
+                __syncwarp();
             }
-        };
-        load_k(0);
-        load_v(0);
-        store_k();
-        tc::fence_proxy_async();
-        mbar_arrive(smem_u32(&tail->k_full));
-        if (tiles > 1) load_k(1);
+            if (last) {
+                if (r < t.rows) {
+                    if (splits == 1)
+                        write_lse(a, at, m, l);
+                    else
+                        *reinterpret_cast<float2 *>(to_part) = make_float2(m, l);
+                }
+                break;
+            }
+            tc::tmem_st_wait();
+            tc::fence_before_sync();
+            mbar_arrive(smem_u32(&tail->block_empty[b & 1]));
+        }
+        tc::fence_before_sync();
+    } else if (warp >= kConvWarp0) {
+        // ------------------------------------------------------------ codes to operands
+        const int tid = threadIdx.x - kConvWarp0 * 32;
         bool ok = true;
         for (int i = 0; i < tiles; ++i) {
-            if (i + 1 < tiles) {
-                ok = mbar_wait_warp(smem_u32(&tail->k_empty), (uint32_t)(i & 1), g.err);
-                if (!ok) break;
-                store_k();
-                tc::fence_proxy_async();
-                mbar_arrive(smem_u32(&tail->k_full));
-                if (i + 2 < tiles) load_k(i + 2);
-            }
-            if (i > 0) ok = mbar_wait_warp(smem_u32(&tail->pv_done), (uint32_t)((i - 1) & 1), g.err);
+            const int s = i % kStages;
+            const uint32_t raw = raw_at + s * 2 * S::kRaw;
+            ok = mbar_wait_warp(smem_u32(&tail->raw_full[s]), (uint32_t)((i / kStages) & 1), g.err);
+            if (ok && i > 1) ok = mbar_wait_warp(smem_u32(&tail->k_empty[i & 1]), (uint32_t)(((i >> 1) & 1) ^ 1), g.err);
             if (!ok) break;
-            store_v();
+#pragma unroll
+            for (int n = 0; n < D / 32; ++n) {
+                const int task = n * kConv + tid;
+                store_k_segment(k_at + (i & 1) * S::kKBytes, task / (D / 16), task % (D / 16), lds128(raw + 16 * task));
+            }
             tc::fence_proxy_async();
-            mbar_arrive(smem_u32(&tail->v_full));
-            if (i + 1 < tiles) load_v(i + 1);
+            mbar_arrive(smem_u32(&tail->k_full[i & 1]));
+            // squares of 8 x 8 codes, along diagonals: no bank twice, neither reading nor writing
+            const int dg = tid % (D / 8), tg = (tid / (D / 8) + dg) & 7;
+            uint2 v[8];
+            if (tid < D) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = lds64(raw + S::kRaw + (8 * tg + k) * D + 8 * dg);
+            }
+            mbar_arrive(smem_u32(&tail->raw_empty[s]));
+            if (i > 1) ok = mbar_wait_warp(smem_u32(&tail->v_empty[i & 1]), (uint32_t)(((i >> 1) & 1) ^ 1), g.err);
+            if (!ok) break;
+            if (tid < D) store_v_square(v_at + (i & 1) * S::kVBytes, tg, dg, v);
+            tc::fence_proxy_async();
+            mbar_arrive(smem_u32(&tail->v_full[i & 1]));
         }
     } else {
         // ------------------------------------------------------------ softmax
-        const int r = threadIdx.x;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
-        const float inf = __int_as_float(0x7F800000);
+        const int half = warp >> 2, r = 32 * (warp & 3) + lane;  // the row, and which 32 of a tile's tokens
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const int pos = t.start + (t.r0 + r) / group;
         const int from = a.window && a.window <= pos ? (int)(pos - a.window + 1) : 0;
         const int to = r >= t.rows ? 0 : a.causal ? pos + 1 : t.s.len;
         const float qf = tail->down[r] * a.scale;
         float m = -inf, l = 0.0f;
-        const int64_t at = (int64_t)(t.s.row0 + (t.r0 + r) / group) * a.q_heads + h * group + (t.r0 + r) % group;
-        float *const to_part = part + (((unit * c.heads + h) * gridDim.z + blockIdx.z) * kRows + r) * (D + 4);
-        // lane q < 4: the scales of the tile's tokens 16 q .. 16 q + 15 (one page)
-        const int32_t *ids = g.table + (int64_t)t.b * g.max_pages;
+        int block = -1, age = 0;  // the block, and tiles in it
+        // even and odd lanes: the scales of the half's first and last 16 tokens (one page each)
         float ks = 0.0f, vs = 0.0f;
         bool held = false;
         auto load_scales = [&](int i) {
-            const int token = begin + i * kTok + 16 * (lane & 3);
+            const int token = begin + i * kTok + kHalf * half + 16 * (lane & 1);
             const int id = token < end ? ids[token >> shift] : -1;
             held = id >= 0 && id < g.num_pages;
             if (held) {
@@ -360,37 +329,34 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
             }
         };
         load_scales(0);
-        bool ok = true;
+        bool ok = true;  // after a timeout the warp only keeps the others' barriers
         for (int i = 0; i < tiles; ++i) {
-            float f[4], lv[4], iv[4];
+            float f[2], lv[2], iv[2];
             {
                 const float ve = vs > 0.0f ? vs : vs == 0.0f ? 5.421010862e-20f : inf;  // zeros: any scale does; NaN as infinity
                 const float lv1 = held ? log2f(ve) : -inf, iv1 = held ? 1.0f / ve : 0.0f, ks1 = held ? ks : 0.0f;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 2; ++q) {
                     f[q] = qf * __shfl_sync(0xffffffffu, ks1, q);
                     lv[q] = __shfl_sync(0xffffffffu, lv1, q);
                     iv[q] = __shfl_sync(0xffffffffu, iv1, q);
                 }
             }
             if (i + 1 < tiles) load_scales(i + 1);
-            __syncwarp();
-            const int t0 = begin + i * kTok;
-            const bool all = __all_sync(0xffffffffu, t0 >= from && t0 + kTok <= to);
-            ok = mbar_wait_warp(smem_u32(&tail->s_full[i & 1]), (uint32_t)((i >> 1) & 1), g.err);
-            if (!ok) break;
+            const int t0 = begin + i * kTok + kHalf * half;
+            const bool all = __all_sync(0xffffffffu, t0 >= from && t0 + kHalf <= to);
+            ok = ok && mbar_wait_warp(smem_u32(&tail->s_full[i & 1]), (uint32_t)((i >> 1) & 1), g.err);
             __syncwarp();
             tc::fence_after_sync();
             const uint32_t sp = lanes + (i & 1) * kTok;
-            float x[kTok];
+            float x[kHalf];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tc::tmem_ld16(sp + 16 * q, *reinterpret_cast<float(*)[16]>(&x[16 * q]));
+            for (int q = 0; q < 2; ++q) tc::tmem_ld16(sp + kHalf * half + 16 * q, *reinterpret_cast<float(*)[16]>(&x[16 * q]));
 #pragma unroll
-            for (int q = 0; q < 4; ++q) ld_wait16(*reinterpret_cast<float(*)[16]>(&x[16 * q]));
-            // u = x f + lv, the largest one that the row sees
-            float most = -inf;
+            for (int q = 0; q < 2; ++q) ld_wait16(*reinterpret_cast<float(*)[16]>(&x[16 * q]));
+            // u = x f + lv, and the largest one that the row sees
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 const uint64_t f2 = pair(f[q], f[q]), lv2 = pair(lv[q], lv[q]);
 #pragma unroll
                 for (int k = 16 * q; k < 16 * q + 16; k += 2) {
@@ -401,37 +367,31 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
             }
             if (!all)
 #pragma unroll
-                for (int k = 0; k < kTok; ++k) x[k] = t0 + k >= from && t0 + k < to ? x[k] : -inf;
+                for (int k = 0; k < kHalf; ++k) x[k] = t0 + k >= from && t0 + k < to ? x[k] : -inf;
+            float most = -inf;
 #pragma unroll
-            for (int k = 0; k < kTok; k += 2) most = max3(most, x[k], x[k + 1]);
-            const bool renew = most > m + kRenew;
-            if (__any_sync(0xffffffffu, renew)) {
-                const float n = renew ? most - kTop : m, scale = m == -inf ? 0.0f : renew ? ex2(m - n) : 1.0f;
-                m = n;
-                l *= scale;
+            for (int k = 0; k < kHalf; k += 2) most = max3(most, x[k], x[k + 1]);
+            tail->most[i & 1][half][r] = most;
+            // (also: both threads of a row have read its scores before either writes weights)
+            const bool renew = any_of_soft(most > m + kRenew);
+            if (i == 0 || renew || (PARTS == 2 && age == kBlock)) {
                 if (i > 0) {
-                    // S(i) came after tile i - 2's values, so at most tile i - 1's are open
-                    ok = mbar_wait_warp(smem_u32(&tail->pv_done), (uint32_t)((i - 1) & 1), g.err);
-                    if (!ok) break;
-                    __syncwarp();
-                    tc::fence_after_sync();
-#pragma unroll 1
-                    for (int d = 0; d < D; d += 16) {
-                        float o[16];
-                        uint32_t w[16];
-                        tc::tmem_ld16(lanes + S::kTmemO + d, o);
-                        ld_wait16(o);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * scale);
-                        tc::tmem_st16(lanes + S::kTmemO + d, w);
-                    }
+                    tail->m[block & 3][r] = m;
+                    tail->l[block & 3][half][r] = l;
                 }
+                ++block;
+                age = 0;
+                l = 0.0f;
+                const float both = fmaxf(tail->most[i & 1][0][r], tail->most[i & 1][1][r]);
+                if (both > -inf) m = both - kTop;
             }
+            if (threadIdx.x == 0) tail->begins[i & 1] = age == 0;
+            ++age;
             const float mm = m == -inf ? 0.0f : -m;
             const uint64_t mm2 = pair(mm, mm);
-            uint32_t hi[kTok / 2], lo[PARTS == 2 ? kTok / 2 : 1];
+            uint32_t hi[kHalf / 2], lo[kHalf / 2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 uint64_t sum = pair(0.0f, 0.0f);
 #pragma unroll
                 for (int k = 16 * q; k < 16 * q + 16; k += 2) {
@@ -443,53 +403,26 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
                 }
                 l = fmaf(unpair(sum).x + unpair(sum).y, iv[q], l);
             }
-            __syncwarp();
-            tc::tmem_st16(sp, *reinterpret_cast<uint32_t(*)[16]>(&hi[0]));
-            tc::tmem_st16(sp + 16, *reinterpret_cast<uint32_t(*)[16]>(&hi[16]));
-            if (PARTS == 2) {
-                tc::tmem_st16(sp + 32, *reinterpret_cast<uint32_t(*)[16]>(&lo[0]));
-                tc::tmem_st16(sp + 48, *reinterpret_cast<uint32_t(*)[16]>(&lo[PARTS == 2 ? 16 : 0]));
+            if (i == tiles - 1) {
+                tail->m[block & 3][r] = m;
+                tail->l[block & 3][half][r] = l;
             }
+            __syncwarp();
+            tc::tmem_st16(sp + 16 * half, hi);
+            if (PARTS == 2) tc::tmem_st16(sp + kHalf + 16 * half, lo);
             tc::tmem_st_wait();
             tc::fence_before_sync();
             mbar_arrive(smem_u32(&tail->p_full[i & 1]));
         }
-        // (not pv_done: two of its phases may be open here)
-        if (ok) ok = mbar_wait_warp(smem_u32(&tail->done), 0, g.err);
-        if (ok) {
-            tc::fence_after_sync();
-#pragma unroll 1
-            for (int d = 0; d < D; d += 16) {
-                float o[16];
-                tc::tmem_ld16(lanes + S::kTmemO + d, o);
-                ld_wait16(o);
-                if (r < t.rows) {
-#pragma unroll
-                    for (int k = 0; k < 16; k += 4) {
-                        const float4 v = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                        if (splits == 1)
-                            write_out(a, at * D + d + k, v, l);
-                        else
-                            *reinterpret_cast<float4 *>(to_part + 4 + d + k) = v;
-                    }
-                }
-                __syncwarp();
-            }
-            if (r < t.rows) {
-                if (splits == 1)
-                    write_lse(a, at, m, l);
-                else
-                    *reinterpret_cast<float2 *>(to_part) = make_float2(m, l);
-            }
-        }
         tc::fence_before_sync();
     }
     __syncthreads();
-    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, S::kTmemCols);
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
 }
 
 template <int D, int PARTS>
 cudaError_t launch_prefill(const Cache &c, const Batch &g, const Rope &r, const Attend &a, const Plan &p, float *part, cudaStream_t s) {
+    static_assert(Shape<D>::bytes(2) <= 227 * 1024, "shared memory");
     static std::atomic<uint64_t> ready{0};
     auto kernel = kv_prefill_kernel<D, PARTS>;
     const cudaError_t e = allow_smem((const void *)kernel, Shape<D>::bytes(2), ready);
@@ -509,8 +442,7 @@ cudaError_t launch_kv_prefill(const Cache &c, const Batch &g, const Rope &r, con
     case 64: return two ? launch_prefill<64, 2>(c, g, r, a, p, part, s) : launch_prefill<64, 1>(c, g, r, a, p, part, s);
     case 96: return two ? launch_prefill<96, 2>(c, g, r, a, p, part, s) : launch_prefill<96, 1>(c, g, r, a, p, part, s);
     case 128: return two ? launch_prefill<128, 2>(c, g, r, a, p, part, s) : launch_prefill<128, 1>(c, g, r, a, p, part, s);
-    case 192: return two ? launch_prefill<192, 2>(c, g, r, a, p, part, s) : launch_prefill<192, 1>(c, g, r, a, p, part, s);
-    default: return two ? launch_prefill<256, 2>(c, g, r, a, p, part, s) : launch_prefill<256, 1>(c, g, r, a, p, part, s);
+    default: return launch_kv_prefill_wide(c, g, r, a, p, part, s);
     }
 }
 

@@ -1,0 +1,164 @@
+// kv_prefill.cuh -- what the tcgen05 attention kernels share: paired fp32
+// arithmetic, TMEM waits, and the operands in shared memory (rows of 64
+// fp16 elements, 128-byte swizzle) made from Q and from codes.
+#pragma once
+
+#include "kv_attention.cuh"
+#include "tc.cuh"
+
+namespace qmm {
+namespace serving {
+
+constexpr int kTok = 64;  // tokens of a tile
+static_assert(kTok == kSplitTokens, "splits at tiles");
+
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Waits for the thread's TMEM loads. Their results pass through, so that no
+// use of them is scheduled before the wait.
+__device__ __forceinline__ void ld_wait16(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                   "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    return v;
+}
+
+// The row's elements as fp16 (one or two parts), each quad stored as (0, 2,
+// 1, 3): the order in which codes_02 gives a word's codes. Two threads a row.
+// down[r]: what undoes the power of two of row r.
+template <int D>
+__device__ __forceinline__ void load_q(const Batch &g, const Rope &rope, const Attend &a, const Cache &c, const Tile &t, int h, int group,
+                                       int q_parts, uint8_t *smem, float *down) {
+    constexpr int kRows = kPrefillRows, kPartBytes = (D + 63) / 64 * kRows * 128;
+    const int r = threadIdx.x >> 1, half = threadIdx.x & 1;
+    const int row = (t.r0 + r) / group, head = h * group + (t.r0 + r) % group;
+    const int64_t at = (int64_t)(t.s.row0 + row) * a.Q.stride + (int64_t)head * D;
+    auto item = [&](int j, float4 &x, float4 &y) {
+        const int2 q = quad_at(rope, j);
+        x = y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < t.rows) {
+            if (a.ft == QMM_F32) {
+                x = load4<QMM_F32>(a.Q.p, at + q.x), y = load4<QMM_F32>(a.Q.p, at + q.y);
+            } else if (a.ft == QMM_F16) {
+                x = load4<QMM_F16>(a.Q.p, at + q.x), y = load4<QMM_F16>(a.Q.p, at + q.y);
+            } else {
+                x = load4<QMM_BF16>(a.Q.p, at + q.x), y = load4<QMM_BF16>(a.Q.p, at + q.y);
+            }
+            rotate_item(rope, j, t.start + row, x, y);
+        }
+        return q;
+    };
+    uint32_t most = 0;
+    for (int j = half; j < D / 8; j += 2) {
+        float4 x, y;
+        item(j, x, y);
+        most = max(max(most, __float_as_uint(x.x) & 0x7FFFFFFFu), __float_as_uint(x.y) & 0x7FFFFFFFu);
+        most = max(max(most, __float_as_uint(x.z) & 0x7FFFFFFFu), __float_as_uint(x.w) & 0x7FFFFFFFu);
+        most = max(max(most, __float_as_uint(y.x) & 0x7FFFFFFFu), __float_as_uint(y.y) & 0x7FFFFFFFu);
+        most = max(max(most, __float_as_uint(y.z) & 0x7FFFFFFFu), __float_as_uint(y.w) & 0x7FFFFFFFu);
+    }
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    const float2 f = row_scale(most);
+    if (half == 0) down[r] = f.y;
+    auto store = [&](int d, float4 v) {
+        v = make_float4(v.x * f.x, v.y * f.x, v.z * f.x, v.w * f.x);
+        uint8_t *to = smem + (d >> 6) * (kRows * 128) + r * 128 + ((((d & 63) >> 3) ^ (r & 7)) << 4) + (d & 4) * 2;
+        const uint32_t h0 = half_pair(v.x, v.z), h1 = half_pair(v.y, v.w);
+        *reinterpret_cast<uint2 *>(to) = make_uint2(h0, h1);
+        if (q_parts == 2) *reinterpret_cast<uint2 *>(to + kPartBytes) = make_uint2(rest_pair(v.x, v.z, h0), rest_pair(v.y, v.w, h1));
+    };
+    for (int j = half; j < D / 8; j += 2) {
+        float4 x, y;
+        const int2 q = item(j, x, y);
+        store(q.x, x);
+        store(q.y, y);
+    }
+}
+
+// 16 codes of a K row (segment `seg` of token `token`) as fp16 into the
+// operand at k_at.
+__device__ __forceinline__ void store_k_segment(uint32_t k_at, int token, int seg, uint4 u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        o[2 * k] = codes_02(w[k]);
+        o[2 * k + 1] = codes_02(w[k] >> 8);
+    }
+    const uint32_t to = k_at + (seg >> 2) * (kTok * 128) + token * 128;
+    const int c0 = 2 * (seg & 3), sw = token & 7;
+    // the upper half of a row's segments store their chunks the other way round: no bank twice
+    if (seg & 4) {
+        sts128(to + (((c0 + 1) ^ sw) << 4), o[4], o[5], o[6], o[7]);
+        sts128(to + ((c0 ^ sw) << 4), o[0], o[1], o[2], o[3]);
+    } else {
+        sts128(to + ((c0 ^ sw) << 4), o[0], o[1], o[2], o[3]);
+        sts128(to + (((c0 + 1) ^ sw) << 4), o[4], o[5], o[6], o[7]);
+    }
+}
+
+// 8 x 8 codes of V (tokens 8 tg .., elements 8 dg ..; v[k] token k's) as fp16,
+// transposed, into the operand at v_at.
+__device__ __forceinline__ void store_v_square(uint32_t v_at, int tg, int dg, const uint2 (&v)[8]) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        // y[q][b]: element 4 half + b of tokens 4q .. 4q + 3 in the order 0, 2, 1, 3
+        uint32_t y[2][4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint32_t w0 = half ? v[4 * q].y : v[4 * q].x, w1 = half ? v[4 * q + 1].y : v[4 * q + 1].x;
+            const uint32_t w2 = half ? v[4 * q + 2].y : v[4 * q + 2].x, w3 = half ? v[4 * q + 3].y : v[4 * q + 3].x;
+            const uint32_t lo01 = __byte_perm(w0, w1, 0x5140), hi01 = __byte_perm(w0, w1, 0x7362);
+            const uint32_t lo23 = __byte_perm(w2, w3, 0x5140), hi23 = __byte_perm(w2, w3, 0x7362);
+            y[q][0] = __byte_perm(lo01, lo23, 0x5140);
+            y[q][1] = __byte_perm(lo01, lo23, 0x7362);
+            y[q][2] = __byte_perm(hi01, hi23, 0x5140);
+            y[q][3] = __byte_perm(hi01, hi23, 0x7362);
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int d = 8 * dg + 4 * half + b;
+            sts128(v_at + d * 128 + ((tg ^ (d & 7)) << 4), codes_02(y[0][b]), codes_02(y[0][b] >> 8), codes_02(y[1][b]),
+                   codes_02(y[1][b] >> 8));
+        }
+    }
+}
+
+cudaError_t launch_kv_prefill_wide(const Cache &c, const Batch &g, const Rope &r, const Attend &a, const Plan &p, float *part,
+                                   cudaStream_t s);
+
+}  // namespace serving
+}  // namespace qmm

@@ -1,0 +1,385 @@
+// kv_prefill.cu -- attention over the paged 8-bit cache for many rows per
+// sequence, on the tcgen05 tensor cores. The mathematics is kv_attention.cu's.
+//
+// A CTA takes 128 rows (new tokens x the query heads that share a cached
+// head), one per TMEM lane, and walks the tokens they see 64 at a time:
+//   S = Q K^T   128 x 64, both operands in shared memory (128-byte swizzle);
+//   P           four warps, a thread per row: S from TMEM, weights, back into
+//               the same TMEM columns as fp16 (or two of them);
+//   O += P V    128 x head_dim, P from TMEM, V^T in shared memory.
+// Four more warps turn the codes into the fp16 operands (K as it lies, V
+// transposed, both exact) while the softmax runs, one thread issues the MMAs.
+// S has two TMEM buffers, so the next tile's scores are taken while this
+// one's weights are computed; two CTAs share an SM (head_dim up to 128), so
+// that the tensor cores work for one while the other waits for its softmax.
+//
+// O stays in TMEM; a row whose reference is renewed (a weight would pass
+// 2^15) has it multiplied there, which is rare. The tensor cores cut their
+// sums off rather than round them, which 8192 tokens add up to 1.7e-5 of the
+// result: for fp32 outputs a call is split so that no O sums more than 1024.
+#include "kv_prefill.cuh"
+
+namespace qmm {
+namespace serving {
+namespace {
+
+constexpr int kRows = kPrefillRows;  // of a CTA
+constexpr int kSoftWarps = 4, kConvWarps = 4;
+constexpr int kConv = kConvWarps * 32;
+constexpr int kMmaWarp = kSoftWarps + kConvWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+static_assert(kSoftWarps * 32 == kRows, "a thread for each row");
+
+// Shared memory: Q (one or two parts), K, V^T, then the rest.
+template <int D>
+struct Shape {
+    static constexpr int kChunks = (D + 63) / 64;  // 64-element slices of a head, 128 bytes a row
+    static constexpr int kQBytes = kChunks * kRows * 128, kKBytes = kChunks * kTok * 128, kVBytes = D * 128;
+    static constexpr int kTmemO = 2 * kTok;  // S and P buffers, then O
+    static constexpr int kTmemCols = kTmemO + D <= 256 ? 256 : 512;
+    static constexpr int kCtas = kTmemCols == 256 ? 2 : 1;
+    static constexpr int bytes(int q_parts) { return q_parts * kQBytes + kKBytes + kVBytes + 1024; }
+    static_assert(bytes(2) <= (kCtas == 2 ? 113 : 227) * 1024, "shared memory");
+};
+
+struct Tail {  // behind the operands
+    uint64_t k_full, k_empty, v_full, pv_done, s_full[2], p_full[2], done;
+    uint32_t tmem;
+    float down[kRows];  // what undoes the power of two of each row of Q
+};
+static_assert(sizeof(Tail) <= 1024, "tail");
+
+// PARTS: fp16 numbers that a weight is given as.
+template <int D, int PARTS>
+__global__ void __launch_bounds__(kThreads, Shape<D>::kCtas)
+    kv_prefill_wide_kernel(const Cache c, const Batch g, const Rope rope, const Attend a, int chunk, int q_parts, float *part) {
+    using S = Shape<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    Tail *tail = reinterpret_cast<Tail *>(smem + q_parts * S::kQBytes + S::kKBytes + S::kVBytes);
+    const uint32_t q_at = base, k_at = base + q_parts * S::kQBytes, v_at = k_at + S::kKBytes;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int h = blockIdx.y, group = a.q_heads / c.heads;
+    const int64_t unit = gridDim.x - 1 - blockIdx.x;  // the rows that see most first
+    const Tile t = tile_of(g, a, c.page, group, kRows, unit);
+    if (t.b < 0) return;
+    const int splits = splits_of(t, chunk, gridDim.z);
+    if ((int)blockIdx.z >= splits) return;
+    const int begin = t.lo + (int)blockIdx.z * chunk;
+    const int end = (int)blockIdx.z == splits - 1 ? t.hi : min(t.hi, begin + chunk);
+    const int tiles = (end - begin + kTok - 1) / kTok;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int shift = 31 - __clz(c.page);
+
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&tail->k_full), kConv);
+        mbar_init(smem_u32(&tail->v_full), kConv);
+        mbar_init(smem_u32(&tail->k_empty), 1);
+        mbar_init(smem_u32(&tail->pv_done), 1);
+        mbar_init(smem_u32(&tail->done), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&tail->s_full[i]), 1);
+            mbar_init(smem_u32(&tail->p_full[i]), kRows);
+        }
+        fence_barrier_init();
+    }
+    __syncwarp();
+    if (warp == kMmaWarp) tc::tmem_alloc(smem_u32(&tail->tmem), S::kTmemCols);
+    if (warp < kMmaWarp) load_q<D>(g, rope, a, c, t, h, group, q_parts, smem, tail->down);
+    tc::fence_proxy_async();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tail->tmem;
+
+    if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = tc::idesc_f16_f32(kRows, kTok), idesc_o = tc::idesc_f16_f32(kRows, D);
+            const uint64_t qd = tc::smem_desc(q_at, 1024, 2), kd = tc::smem_desc(k_at, 1024, 2), vd = tc::smem_desc(v_at, 1024, 2);
+            // Tile i's scores go where the weights of tile i - 2 lie: those must
+            // have been used (MMAs of different shapes keep no order).
+            auto scores = [&](int i) {
+                if (i > 1 && !mbar_wait(smem_u32(&tail->pv_done), (uint32_t)(i & 1), g.err)) return false;
+                if (!mbar_wait(smem_u32(&tail->k_full), (uint32_t)(i & 1), g.err)) return false;
+                tc::fence_after_sync();
+                for (int p = 0; p < q_parts; ++p)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc::mma_f16(tmem + (i & 1) * kTok, qd + ((p * S::kQBytes + (k >> 2) * (kRows * 128)) >> 4) + 2 * (k & 3),
+                                    kd + (((k >> 2) * (kTok * 128)) >> 4) + 2 * (k & 3), idesc_s, (p | k) != 0);
+                tc::commit(smem_u32(&tail->k_empty));
+                tc::commit(smem_u32(&tail->s_full[i & 1]));
+                return true;
+            };
+            bool ok = scores(0);
+            for (int i = 0; i < tiles && ok; ++i) {
+                if (i + 1 < tiles) ok = scores(i + 1);
+                ok = ok && mbar_wait(smem_u32(&tail->v_full), (uint32_t)(i & 1), g.err) &&
+                     mbar_wait(smem_u32(&tail->p_full[i & 1]), (uint32_t)((i >> 1) & 1), g.err);
+                if (!ok) break;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                    for (int k = 0; k < kTok / 16; ++k)
+                        tc::mma_f16_ta(tmem + S::kTmemO, tmem + (i & 1) * kTok + p * (kTok / 2) + 8 * k, vd + 2 * k, idesc_o,
+                                       (i | p | k) != 0);
+                tc::commit(smem_u32(&tail->pv_done));
+            }
+            tc::commit(smem_u32(&tail->done));
+            mbar_wait(smem_u32(&tail->done), 0, g.err);  // no MMA may run when TMEM is freed
+        }
+        __syncwarp();
+    } else if (warp >= kSoftWarps) {
+        // ------------------------------------------------------------ codes to operands
+        const int tid = threadIdx.x - kSoftWarps * 32;
+        constexpr int kKLoads = D / 32;                // 16 codes each: D / 16 a token, 64 tokens
+        constexpr int kVLoads = (D + kConv - 1) / kConv;  // 8 x 8 codes each: D / 8 times 8
+        const int32_t *ids = g.table + (int64_t)t.b * g.max_pages;
+        // codes of a token, null where there is none
+        auto codes = [&](const int8_t *p, int token) -> const int8_t * {
+            if (token >= end) return nullptr;
+            const int id = ids[token >> shift];
+            if (id < 0 || id >= g.num_pages) {
+                atomicOr(g.err, kDevErrRange);
+                return nullptr;
+            }
+            return p + (((int64_t)id * c.heads + h) * c.page + (token & (c.page - 1))) * D;
+        };
+        uint4 kr[kKLoads];
+        uint2 vr[kVLoads][8];
+        auto load_k = [&](int i) {
+#pragma unroll
+            for (int n = 0; n < kKLoads; ++n) {
+                const int task = n * kConv + tid, token = task / (D / 16), seg = task % (D / 16);
+                const int8_t *p = codes(c.k, begin + i * kTok + token);
+                kr[n] = p ? ld128(p + 16 * seg) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        auto store_k = [&]() {
+#pragma unroll
+            for (int n = 0; n < kKLoads; ++n) {
+                const int task = n * kConv + tid, token = task / (D / 16), seg = task % (D / 16);
+                store_k_segment(k_at, token, seg, kr[n]);
+            }
+        };
+        auto load_v = [&](int i) {
+#pragma unroll
+            for (int n = 0; n < kVLoads; ++n) {
+                const int task = n * kConv + tid, tg = task & 7, dg = task >> 3;
+                // eight tokens from a multiple of eight on: one page
+                const int token = begin + i * kTok + 8 * tg;
+                const int8_t *p = dg < D / 8 ? codes(c.v, token) : nullptr;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) vr[n][k] = p && token + k < end ? ld64(p + k * D + 8 * dg) : make_uint2(0, 0);
+            }
+        };
+        auto store_v = [&]() {
+#pragma unroll
+            for (int n = 0; n < kVLoads; ++n) {
+                const int task = n * kConv + tid, tg = task & 7, dg = task >> 3;
+                if (dg < D / 8) store_v_square(v_at, tg, dg, vr[n]);
+            }
+        };
+        load_k(0);
+        load_v(0);
+        store_k();
+        tc::fence_proxy_async();
+        mbar_arrive(smem_u32(&tail->k_full));
+        if (tiles > 1) load_k(1);
+        bool ok = true;
+        for (int i = 0; i < tiles; ++i) {
+            if (i + 1 < tiles) {
+                ok = mbar_wait_warp(smem_u32(&tail->k_empty), (uint32_t)(i & 1), g.err);
+                if (!ok) break;
+                store_k();
+                tc::fence_proxy_async();
+                mbar_arrive(smem_u32(&tail->k_full));
+                if (i + 2 < tiles) load_k(i + 2);
+            }
+            if (i > 0) ok = mbar_wait_warp(smem_u32(&tail->pv_done), (uint32_t)((i - 1) & 1), g.err);
+            if (!ok) break;
+            store_v();
+            tc::fence_proxy_async();
+            mbar_arrive(smem_u32(&tail->v_full));
+            if (i + 1 < tiles) load_v(i + 1);
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int r = threadIdx.x;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+        const float inf = __int_as_float(0x7F800000);
+        const int pos = t.start + (t.r0 + r) / group;
+        const int from = a.window && a.window <= pos ? (int)(pos - a.window + 1) : 0;
+        const int to = r >= t.rows ? 0 : a.causal ? pos + 1 : t.s.len;
+        const float qf = tail->down[r] * a.scale;
+        float m = -inf, l = 0.0f;
+        const int64_t at = (int64_t)(t.s.row0 + (t.r0 + r) / group) * a.q_heads + h * group + (t.r0 + r) % group;
+        float *const to_part = part + (((unit * c.heads + h) * gridDim.z + blockIdx.z) * kRows + r) * (D + 4);
+        // lane q < 4: the scales of the tile's tokens 16 q .. 16 q + 15 (one page)
+        const int32_t *ids = g.table + (int64_t)t.b * g.max_pages;
+        float ks = 0.0f, vs = 0.0f;
+        bool held = false;
+        auto load_scales = [&](int i) {
+            const int token = begin + i * kTok + 16 * (lane & 3);
+            const int id = token < end ? ids[token >> shift] : -1;
+            held = id >= 0 && id < g.num_pages;
+            if (held) {
+                ks = c.ks[(int64_t)id * c.heads + h];
+                vs = c.vs[(int64_t)id * c.heads + h];
+            }
+        };
+        load_scales(0);
+        bool ok = true;
+        for (int i = 0; i < tiles; ++i) {
+            float f[4], lv[4], iv[4];
+            {
+                const float ve = vs > 0.0f ? vs : vs == 0.0f ? 5.421010862e-20f : inf;  // zeros: any scale does; NaN as infinity
+                const float lv1 = held ? log2f(ve) : -inf, iv1 = held ? 1.0f / ve : 0.0f, ks1 = held ? ks : 0.0f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    f[q] = qf * __shfl_sync(0xffffffffu, ks1, q);
+                    lv[q] = __shfl_sync(0xffffffffu, lv1, q);
+                    iv[q] = __shfl_sync(0xffffffffu, iv1, q);
+                }
+            }
+            if (i + 1 < tiles) load_scales(i + 1);
+            __syncwarp();
+            const int t0 = begin + i * kTok;
+            const bool all = __all_sync(0xffffffffu, t0 >= from && t0 + kTok <= to);
+            ok = mbar_wait_warp(smem_u32(&tail->s_full[i & 1]), (uint32_t)((i >> 1) & 1), g.err);
+            if (!ok) break;
+            __syncwarp();
+            tc::fence_after_sync();
+            const uint32_t sp = lanes + (i & 1) * kTok;
+            float x[kTok];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tc::tmem_ld16(sp + 16 * q, *reinterpret_cast<float(*)[16]>(&x[16 * q]));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ld_wait16(*reinterpret_cast<float(*)[16]>(&x[16 * q]));
+            // u = x f + lv, the largest one that the row sees
+            float most = -inf;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint64_t f2 = pair(f[q], f[q]), lv2 = pair(lv[q], lv[q]);
+#pragma unroll
+                for (int k = 16 * q; k < 16 * q + 16; k += 2) {
+                    const float2 u = unpair(fma2(pair(x[k], x[k + 1]), f2, lv2));
+                    x[k] = u.x;
+                    x[k + 1] = u.y;
+                }
+            }
+            if (!all)
+#pragma unroll
+                for (int k = 0; k < kTok; ++k) x[k] = t0 + k >= from && t0 + k < to ? x[k] : -inf;
+#pragma unroll
+            for (int k = 0; k < kTok; k += 2) most = max3(most, x[k], x[k + 1]);
+            const bool renew = most > m + kRenew;
+            if (__any_sync(0xffffffffu, renew)) {
+                const float n = renew ? most - kTop : m, scale = m == -inf ? 0.0f : renew ? ex2(m - n) : 1.0f;
+                m = n;
+                l *= scale;
+                if (i > 0) {
+                    // S(i) came after tile i - 2's values, so at most tile i - 1's are open
+                    ok = mbar_wait_warp(smem_u32(&tail->pv_done), (uint32_t)((i - 1) & 1), g.err);
+                    if (!ok) break;
+                    __syncwarp();
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int d = 0; d < D; d += 16) {
+                        float o[16];
+                        uint32_t w[16];
+                        tc::tmem_ld16(lanes + S::kTmemO + d, o);
+                        ld_wait16(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * scale);
+                        tc::tmem_st16(lanes + S::kTmemO + d, w);
+                    }
+                }
+            }
+            const float mm = m == -inf ? 0.0f : -m;
+            const uint64_t mm2 = pair(mm, mm);
+            uint32_t hi[kTok / 2], lo[PARTS == 2 ? kTok / 2 : 1];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint64_t sum = pair(0.0f, 0.0f);
+#pragma unroll
+                for (int k = 16 * q; k < 16 * q + 16; k += 2) {
+                    const float2 d = unpair(add2(pair(x[k], x[k + 1]), mm2));
+                    const float w0 = ex2(d.x), w1 = ex2(d.y);
+                    sum = add2(sum, pair(w0, w1));
+                    hi[k / 2] = half_pair(w0, w1);
+                    if (PARTS == 2) lo[k / 2] = rest_pair(w0, w1, hi[k / 2]);
+                }
+                l = fmaf(unpair(sum).x + unpair(sum).y, iv[q], l);
+            }
+            __syncwarp();
+            tc::tmem_st16(sp, *reinterpret_cast<uint32_t(*)[16]>(&hi[0]));
+            tc::tmem_st16(sp + 16, *reinterpret_cast<uint32_t(*)[16]>(&hi[16]));
+            if (PARTS == 2) {
+                tc::tmem_st16(sp + 32, *reinterpret_cast<uint32_t(*)[16]>(&lo[0]));
+                tc::tmem_st16(sp + 48, *reinterpret_cast<uint32_t(*)[16]>(&lo[PARTS == 2 ? 16 : 0]));
+            }
+            tc::tmem_st_wait();
+            tc::fence_before_sync();
+            mbar_arrive(smem_u32(&tail->p_full[i & 1]));
+        }
+        // (not pv_done: two of its phases may be open here)
+        if (ok) ok = mbar_wait_warp(smem_u32(&tail->done), 0, g.err);
+        if (ok) {
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int d = 0; d < D; d += 16) {
+                float o[16];
+                tc::tmem_ld16(lanes + S::kTmemO + d, o);
+                ld_wait16(o);
+                if (r < t.rows) {
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        const float4 v = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        if (splits == 1)
+                            write_out(a, at * D + d + k, v, l);
+                        else
+                            *reinterpret_cast<float4 *>(to_part + 4 + d + k) = v;
+                    }
+                }
+                __syncwarp();
+            }
+            if (r < t.rows) {
+                if (splits == 1)
+                    write_lse(a, at, m, l);
+                else
+                    *reinterpret_cast<float2 *>(to_part) = make_float2(m, l);
+            }
+        }
+        tc::fence_before_sync();
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, S::kTmemCols);
+}
+
+template <int D, int PARTS>
+cudaError_t launch_wide(const Cache &c, const Batch &g, const Rope &r, const Attend &a, const Plan &p, float *part, cudaStream_t s) {
+    static std::atomic<uint64_t> ready{0};
+    auto kernel = kv_prefill_wide_kernel<D, PARTS>;
+    const cudaError_t e = allow_smem((const void *)kernel, Shape<D>::bytes(2), ready);
+    if (e != cudaSuccess) return e;
+    // 16-bit elements are exact in one fp16 number (bf16's after the power of two); fp32 and rotated ones take two
+    const int q_parts = a.ft == QMM_F32 || r.dim ? 2 : 1;
+    const dim3 grid((unsigned)p.units, (unsigned)c.heads, (unsigned)p.splits);
+    return launch(kernel, grid, kThreads, (size_t)Shape<D>::bytes(q_parts), s, c, g, r, a, p.chunk, q_parts, part);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_prefill_wide(const Cache &c, const Batch &g, const Rope &r, const Attend &a, const Plan &p, float *part,
+                                   cudaStream_t s) {
+    const bool two = a.ft == QMM_F32;
+    if (c.dim == 192) return two ? launch_wide<192, 2>(c, g, r, a, p, part, s) : launch_wide<192, 1>(c, g, r, a, p, part, s);
+    return two ? launch_wide<256, 2>(c, g, r, a, p, part, s) : launch_wide<256, 1>(c, g, r, a, p, part, s);
+}
+
+}  // namespace serving
+}  // namespace qmm
