@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, D <= 128 && NT == 1 ? 4 : 1)
             const float ve = v > 0.0f ? v : v == 0.0f ? 5.421010862e-20f : inf;  // zeros: any scale does; NaN as infinity
             sm.id[i] = id;
             sm.ks[i] = c.ks[at];
-            sm.lv[i] = log2f(ve);
-            sm.iv[i] = 1.0f / ve;
+            sm.lv[i] = lg2(ve);
+            sm.iv[i] = inverse(ve);
         }
         __syncthreads();
 
@@ -450,8 +450,9 @@ __global__ void __launch_bounds__(kJoinThreads)
     write_out(a, at * D + d, o, l);
 }
 
-// Tokens that kv_prefill_wide.cu's tensor cores may sum for an fp32 output.
-constexpr int64_t kSumTokens = 512;
+// Tokens that kv_prefill_wide.cu's tensor cores may sum for an fp32 and for a
+// 16-bit output.
+constexpr int64_t kSumTokens = 512, kSumTokens16 = 8192;
 // Rows of a sequence up to which a tile is eight or sixteen of them.
 constexpr int64_t kFewRows = 64;
 // Splits of few rows join in a (portable) cluster where all CTAs run at once:
@@ -486,7 +487,10 @@ Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_
     // a short cache is read sooner than a second kernel starts
     if (p.tile_rows != kPrefillRows && kv <= kClusterTokens && splits > kClusterMax) splits = kClusterMax;
     if (splits > 256) splits = 256;
-    if (p.tile_rows == kPrefillRows && dim > 128 && ft == QMM_F32 && splits < (kv + kSumTokens - 1) / kSumTokens) splits = (kv + kSumTokens - 1) / kSumTokens;
+    if (p.tile_rows == kPrefillRows && (ft != QMM_F32 || dim > 128)) {
+        const int64_t sum = ft == QMM_F32 ? kSumTokens : kSumTokens16;
+        if (splits < (kv + sum - 1) / sum) splits = (kv + sum - 1) / sum;
+    }
     p.chunk = (int)(((kv + splits - 1) / splits + kSplitTokens - 1) / kSplitTokens * kSplitTokens);
     p.splits = (int)((kv + p.chunk - 1) / p.chunk);
     p.cluster = joins_in_cluster(p, ctas);
@@ -513,8 +517,13 @@ cudaError_t launch_tiles(const Cache &c, const Batch &g, const Rope &r, const At
 size_t kv_attention_bytes(int heads, int dim, int page, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv) {
     (void)page;
     // for any window: a window only lowers the number of splits' tokens, not their bound
-    const Plan p = plan_of(heads, dim, batch, q_heads, T, max_q, max_kv, 0, QMM_F32);
-    return p.splits == 1 || p.cluster ? 0 : (size_t)p.units * heads * p.splits * p.tile_rows * (dim + 4) * 4;
+    size_t most = 0;
+    for (const int ft : {QMM_F32, QMM_F16}) {
+        const Plan p = plan_of(heads, dim, batch, q_heads, T, max_q, max_kv, 0, ft);
+        const size_t bytes = p.splits == 1 || p.cluster ? 0 : (size_t)p.units * heads * p.splits * p.tile_rows * (dim + 4) * 4;
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 cudaError_t launch_kv_attention(const Cache &c, const Batch &g, const Rope &r, const Attend &a, void *ws, cudaStream_t s) {

@@ -17,6 +17,18 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// One-instruction log2 and inverse of a page scale, each within 2^-22: only
+// their agreement matters, a page's weights in O against those in l.
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float inverse(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // Bytes 0 and 2 of x, signed codes, as two exact fp16 numbers: byte ^ 0x80
 // under the exponent of 1024 is 1152 + code.
 __device__ __forceinline__ uint32_t codes_02(uint32_t x) {

@@ -1,6 +1,6 @@
 // kv_prefill.cu -- attention over the paged 8-bit cache for many rows per
-// sequence, on the tcgen05 tensor cores, for head_dim up to 128. The
-// mathematics is kv_attention.cu's.
+// sequence, on the tcgen05 tensor cores, for fp32 Q and a head_dim up to 128
+// (kv_prefill_wide.cu has the others). The mathematics is kv_attention.cu's.
 //
 // A CTA takes 128 rows (new tokens x the query heads that share a cached
 // head), one per TMEM lane, and walks the tokens they see 64 at a time, as a
@@ -12,11 +12,11 @@
 //   MMA issuer   S = Q K^T (128 x 64) into one of two TMEM buffers; O += P V
 //                (128 x head_dim), P from TMEM;
 //   softmax      eight warps, two threads a row: S from TMEM, weights, back
-//                into the same columns as one or two fp16 numbers;
+//                into the same columns as two fp16 numbers;
 //   joiners      four warps, a thread a row, see below.
 // The next tile's scores are taken while this one's weights are computed, so
 // the tensor cores are what bounds it (2 x head_dim x 64 x 128 products a
-// tile, twice each where Q and P are two numbers).
+// tile, twice each as Q and P are two fp16 numbers).
 //
 // The tensor cores cut their sums off rather than round them: over 8192 tokens
 // in one accumulator, 1.7e-5 of the result. So the tiles come in blocks of
@@ -40,6 +40,7 @@ constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kStages = 4;  // tiles of codes on their way
 constexpr int kBlock = 8;   // tiles that share an O: their cut-off stays below 1e-6
 constexpr int kHalf = kTok / 2;
+constexpr int kParts = 2;   // fp16 numbers that an element of Q and a weight are given as
 static_assert(kSoft == 2 * kRows && kJoin == kRows, "threads of a row");
 
 struct Tail {  // behind the operands
@@ -60,7 +61,7 @@ struct Shape {
     static constexpr int kRaw = kTok * D;  // codes of K, or of V, of a tile
     static constexpr int kBlockCol = 2 * kTok, kWholeCol = kBlockCol + 2 * D;  // TMEM: S and P, O of two blocks, the whole O
     static_assert(kWholeCol + D <= 512, "TMEM");
-    static constexpr int bytes(int q_parts) { return q_parts * kQBytes + 2 * (kKBytes + kVBytes) + kStages * 2 * kRaw + (int)sizeof(Tail); }
+    static constexpr int kBytes = kParts * kQBytes + 2 * (kKBytes + kVBytes) + kStages * 2 * kRaw + (int)sizeof(Tail);
 };
 
 // Whether any of the softmax threads says yes; a barrier among them.
@@ -73,14 +74,13 @@ __device__ __forceinline__ bool any_of_soft(bool yes) {
     return r != 0;
 }
 
-// PARTS: fp16 numbers that a weight is given as.
-template <int D, int PARTS>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv_prefill_kernel(const Cache c, const Batch g, const Rope rope, const Attend a, int chunk, int q_parts, float *part) {
+    kv_prefill_kernel(const Cache c, const Batch g, const Rope rope, const Attend a, int chunk, float *part) {
     using S = Shape<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
-    const uint32_t q_at = base, k_at = q_at + q_parts * S::kQBytes, v_at = k_at + 2 * S::kKBytes, raw_at = v_at + 2 * S::kVBytes;
+    const uint32_t q_at = base, k_at = q_at + kParts * S::kQBytes, v_at = k_at + 2 * S::kKBytes, raw_at = v_at + 2 * S::kVBytes;
     Tail *tail = reinterpret_cast<Tail *>(smem + (raw_at - base) + kStages * 2 * S::kRaw);
     pdl_launch_dependents();
     pdl_wait();
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     if (warp == kMmaWarp) tc::tmem_alloc(smem_u32(&tail->tmem), 512);
-    if (warp < kSoftWarps) load_q<D>(g, rope, a, c, t, h, group, q_parts, smem, tail->down);
+    if (warp < kSoftWarps) load_q<D>(g, rope, a, c, t, h, group, kParts, smem, tail->down);
     tc::fence_proxy_async();
     tc::fence_before_sync();
     __syncthreads();
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!mbar_wait(smem_u32(&tail->k_full[i & 1]), (uint32_t)((i >> 1) & 1), g.err)) return false;
                 tc::fence_after_sync();
                 const uint64_t kb = kd + (((i & 1) * S::kKBytes) >> 4);
-                for (int p = 0; p < q_parts; ++p)
+                for (int p = 0; p < kParts; ++p)
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         tc::mma_f16(tmem + (i & 1) * kTok, qd + ((p * S::kQBytes + (k >> 2) * (kRows * 128)) >> 4) + 2 * (k & 3),
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after_sync();
                 const uint64_t vb = vd + (((i & 1) * S::kVBytes) >> 4);
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p)
+                for (int p = 0; p < kParts; ++p)
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k)
                         tc::mma_f16_ta(tmem + S::kBlockCol + (block & 1) * D, tmem + (i & 1) * kTok + p * kHalf + 8 * k, vb + 2 * k,
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tail->most[i & 1][half][r] = most;
             // (also: both threads of a row have read its scores before either writes weights)
             const bool renew = any_of_soft(most > m + kRenew);
-            if (i == 0 || renew || (PARTS == 2 && age == kBlock)) {
+            if (i == 0 || renew || age == kBlock) {
                 if (i > 0) {
                     tail->m[block & 3][r] = m;
                     tail->l[block & 3][half][r] = l;
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 age = 0;
                 l = 0.0f;
                 const float both = fmaxf(tail->most[i & 1][0][r], tail->most[i & 1][1][r]);
-                if (both > -inf) m = both - kTop;
+                if (both > -inf) m = fmaxf(m, both - kTop);  // never lower: it would soon be renewed again
             }
             if (threadIdx.x == 0) tail->begins[i & 1] = age == 0;
             ++age;
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float w0 = ex2(d.x), w1 = ex2(d.y);
                     sum = add2(sum, pair(w0, w1));
                     hi[k / 2] = half_pair(w0, w1);
-                    if (PARTS == 2) lo[k / 2] = rest_pair(w0, w1, hi[k / 2]);
+                    lo[k / 2] = rest_pair(w0, w1, hi[k / 2]);
                 }
                 l = fmaf(unpair(sum).x + unpair(sum).y, iv[q], l);
             }
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             tc::tmem_st16(sp + 16 * half, hi);
-            if (PARTS == 2) tc::tmem_st16(sp + kHalf + 16 * half, lo);
+            tc::tmem_st16(sp + kHalf + 16 * half, lo);
             tc::tmem_st_wait();
             tc::fence_before_sync();
             mbar_arrive(smem_u32(&tail->p_full[i & 1]));
@@ -420,28 +420,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
 }
 
-template <int D, int PARTS>
+template <int D>
 cudaError_t launch_prefill(const Cache &c, const Batch &g, const Rope &r, const Attend &a, const Plan &p, float *part, cudaStream_t s) {
-    static_assert(Shape<D>::bytes(2) <= 227 * 1024, "shared memory");
+    static_assert(Shape<D>::kBytes <= 227 * 1024, "shared memory");
     static std::atomic<uint64_t> ready{0};
-    auto kernel = kv_prefill_kernel<D, PARTS>;
-    const cudaError_t e = allow_smem((const void *)kernel, Shape<D>::bytes(2), ready);
+    auto kernel = kv_prefill_kernel<D>;
+    const cudaError_t e = allow_smem((const void *)kernel, Shape<D>::kBytes, ready);
     if (e != cudaSuccess) return e;
-    // 16-bit elements are exact in one fp16 number (bf16's after the power of two); fp32 and rotated ones take two
-    const int q_parts = a.ft == QMM_F32 || r.dim ? 2 : 1;
     const dim3 grid((unsigned)p.units, (unsigned)c.heads, (unsigned)p.splits);
-    return launch(kernel, grid, kThreads, (size_t)Shape<D>::bytes(q_parts), s, c, g, r, a, p.chunk, q_parts, part);
+    return launch(kernel, grid, kThreads, (size_t)Shape<D>::kBytes, s, c, g, r, a, p.chunk, part);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_prefill(const Cache &c, const Batch &g, const Rope &r, const Attend &a, const Plan &p, float *part,
                               cudaStream_t s) {
-    const bool two = a.ft == QMM_F32;
+    if (a.ft != QMM_F32) return launch_kv_prefill_wide(c, g, r, a, p, part, s);
     switch (c.dim) {
-    case 64: return two ? launch_prefill<64, 2>(c, g, r, a, p, part, s) : launch_prefill<64, 1>(c, g, r, a, p, part, s);
-    case 96: return two ? launch_prefill<96, 2>(c, g, r, a, p, part, s) : launch_prefill<96, 1>(c, g, r, a, p, part, s);
-    case 128: return two ? launch_prefill<128, 2>(c, g, r, a, p, part, s) : launch_prefill<128, 1>(c, g, r, a, p, part, s);
+    case 64: return launch_prefill<64>(c, g, r, a, p, part, s);
+    case 96: return launch_prefill<96>(c, g, r, a, p, part, s);
+    case 128: return launch_prefill<128>(c, g, r, a, p, part, s);
     default: return launch_kv_prefill_wide(c, g, r, a, p, part, s);
     }
 }

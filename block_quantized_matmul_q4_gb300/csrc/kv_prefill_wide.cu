@@ -1,5 +1,6 @@
-// kv_prefill.cu -- attention over the paged 8-bit cache for many rows per
-// sequence, on the tcgen05 tensor cores. The mathematics is kv_attention.cu's.
+// kv_prefill_wide.cu -- attention over the paged 8-bit cache for many rows per
+// sequence, on the tcgen05 tensor cores: 16-bit Q, or a head_dim above 128.
+// The mathematics is kv_attention.cu's.
 //
 // A CTA takes 128 rows (new tokens x the query heads that share a cached
 // head), one per TMEM lane, and walks the tokens they see 64 at a time:
@@ -16,7 +17,11 @@
 // O stays in TMEM; a row whose reference is renewed (a weight would pass
 // 2^15) has it multiplied there, which is rare. The tensor cores cut their
 // sums off rather than round them, which 8192 tokens add up to 1.7e-5 of the
-// result: for fp32 outputs a call is split so that no O sums more than 1024.
+// result: a split sums at most that many for a 16-bit output, and 512 (below
+// 3e-6) for an fp32 one. kv_prefill.cu, which sums in blocks instead, has one
+// CTA an SM and more waiting: 16-bit prompts take it longer (7 of up to 600
+// tokens over 1500, head_dim 64, bf16: 103 us against 77), fp32 ones at
+// head_dim 128 would take this one longer (the splits' parts to and fro).
 #include "kv_prefill.cuh"
 
 namespace qmm {
@@ -376,9 +381,14 @@ cudaError_t launch_wide(const Cache &c, const Batch &g, const Rope &r, const Att
 
 cudaError_t launch_kv_prefill_wide(const Cache &c, const Batch &g, const Rope &r, const Attend &a, const Plan &p, float *part,
                                    cudaStream_t s) {
-    const bool two = a.ft == QMM_F32;
-    if (c.dim == 192) return two ? launch_wide<192, 2>(c, g, r, a, p, part, s) : launch_wide<192, 1>(c, g, r, a, p, part, s);
-    return two ? launch_wide<256, 2>(c, g, r, a, p, part, s) : launch_wide<256, 1>(c, g, r, a, p, part, s);
+    const bool two = a.ft == QMM_F32;  // (then only with head_dim above 128)
+    switch (c.dim) {
+    case 64: return launch_wide<64, 1>(c, g, r, a, p, part, s);
+    case 96: return launch_wide<96, 1>(c, g, r, a, p, part, s);
+    case 128: return launch_wide<128, 1>(c, g, r, a, p, part, s);
+    case 192: return two ? launch_wide<192, 2>(c, g, r, a, p, part, s) : launch_wide<192, 1>(c, g, r, a, p, part, s);
+    default: return two ? launch_wide<256, 2>(c, g, r, a, p, part, s) : launch_wide<256, 1>(c, g, r, a, p, part, s);
+    }
 }
 
 }  // namespace serving

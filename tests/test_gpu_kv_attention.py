@@ -233,3 +233,37 @@ def test_cache_past_32_bit_offsets(q):  # noqa: F811
     got, want = k[0, :, :rows].cpu().numpy(), c.x[0][-rows:].transpose(1, 0, 2)
     d = bs[0][last].cpu().numpy()[:, None, None]
     assert np.all(np.abs(got - want) <= 0.51 * d) and math.isfinite(got.sum())
+
+
+@pytest.mark.parametrize("dim,page,rot", [(192, 32, 192), (256, 64, 0), (96, 16, 32), (128, 32, 128)])
+def test_prompts_of_fp32_heads(q, dim, page, rot):  # noqa: F811
+    """Two fp16 numbers each for Q and the weights at every width, over more than one split's tokens."""
+    c = Case(q, [(150, 1300), (40, 40), (1, 600), (90, 91)], 2, page, dim, seed=dim)
+    x = inputs(c, 8, "f32")
+    table = rope_table(c.most * page, rot) if rot else None
+    out, lse = call(q, c, x, q.Rope(torch.from_numpy(table).cuda()) if rot else None)
+    rows = set(range(0, c.rows, 17)) | {int(f) - 1 for f in c.first[1:]}
+    check(c, x, "f32", out, lse, rows=rows, table=table)
+
+
+@pytest.mark.parametrize("dim,kind,window", [(128, "f32", 0), (64, "f32", 0), (128, "f16", 0), (64, "bf16", 500), (192, "f32", 0), (256, "bf16", 0)])
+def test_long_prompts_agree_with_decode(q, dim, kind, window):  # noqa: F811
+    """Thousands of tiles on the prompts' kernels against every row on the single tokens' one.
+
+    Both are within the bound of the exact result, so within two of each other, with sum p |v| at most
+    the largest |v| and sum |q| |k| at most |q|_1 max |k|."""
+    c = Case(q, [(700, 2500), (1300, 1300), (64, 5000), (3, 9), (0, 7), (500, 9000)], 2, 32, dim, seed=dim)
+    x = inputs(c, 16, kind)
+    key, value = values(c)
+    xs = c.dim ** -0.5 * float(x.double().abs().sum(-1).max()) * float(np.abs(key).max())
+    top = float(np.abs(value).max())
+    e = (2.0 ** -18 + 2.0 ** -21) * xs
+    rel = 2 * e + 2.0 ** -19 + 9000 * 2.0 ** -24 + (0 if kind == "f32" else 2.0 ** -11)
+    a, la = call(q, c, x, window=window)
+    for _ in range(3):
+        again, lagain = call(q, c, x, window=window)
+        assert torch.equal(a, again) and torch.equal(la, lagain)
+    b, lb = call(q, c, x, window=window, max_q=1)
+    a, b = a.double(), b.double()
+    assert ((a - b).abs() <= 2 * (rel * top + EPS[kind] * (b.abs() + rel * top))).all()
+    assert ((la - lb).abs() <= 2 * (e + 2.0 ** -20 + 2.0 ** -22 * lb.abs())).all()
