@@ -3,21 +3,23 @@
 //
 // A block is one page of one head. Its scale is a running maximum, so a block
 // that grows re-rounds the codes that it holds: q' = round(q d_old / d). One
-// CTA owns a block for the whole call, which makes the maximum, the re-rounding
-// and the new codes one pass: the new values (at most page_tokens * head_dim,
-// eight pairs' worth of registers for each thread) are read from memory once,
-// rotated, reduced to their largest magnitude and written as codes. Both
-// kernels are bound by memory traffic for prompts and by the chain of
-// dependent loads (row offsets, page id, scale) for a decode step.
+// CTA, or one warp where a call has few rows for each sequence, owns a block
+// for the whole call, which makes the maximum, the re-rounding and the new
+// codes one pass without atomics. All are bound by memory traffic where there
+// is much of it and by their chain of dependent loads (row offsets; page id
+// and new rows; scale) where there is little: each link's loads are issued
+// together, and nothing waits that the next link does not need.
 #include "serving.cuh"
 
 namespace qmm {
 namespace serving {
 namespace {
 
-constexpr int kItems = 8;     // items of eight elements that a thread holds
 constexpr int kThreadsMax = 512;
-static_assert(kThreadsMax * kItems * 8 >= kPageMax * kHeadDimMax, "a block fits its CTA's registers");
+// Rows that a thread of a CTA holds (one item of eight elements of each): four,
+// or eight of the largest blocks, whose threads would not fit a CTA.
+constexpr int held_rows(int page, int dim) { return page * dim / 32 <= kThreadsMax ? 4 : 8; }
+static_assert(kPageMax * kHeadDimMax / 64 <= kThreadsMax, "a block fits its CTA's registers");
 
 __device__ __forceinline__ int code_of(float x, float inv) { return q8_code(x, inv); }
 __device__ __forceinline__ uint32_t pack_codes(float4 v, float inv) {
@@ -33,9 +35,62 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t m, float4 v) {
     return max(m, __float_as_uint(v.w) & 0x7FFFFFFFu);
 }
 
-// grid: (units, heads, keys or values). Unit = one page that a sequence
-// appends to.
-template <int FT>
+// What a block's scale becomes.
+struct Scale {
+    float d, inv;
+    bool grew, plain;  // plain: neither zero nor infinite
+};
+__device__ __forceinline__ Scale scale_of(uint32_t most, float d_old) {
+    const float inf = __int_as_float(0x7F800000);
+    Scale s;
+    s.d = most >= 0x7F800000u ? inf : __fdiv_rn(__uint_as_float(most), 127.0f);
+    if (s.d < 1.17549435e-38f) s.d = 0.0f;  // 1 / d would overflow
+    s.grew = s.d > d_old;
+    if (!s.grew) s.d = d_old;
+    s.plain = s.d > 0.0f && s.d < inf;
+    s.inv = s.plain ? __fdiv_rn(1.0f, s.d) : 0.0f;
+    return s;
+}
+__device__ __forceinline__ void store_item(int8_t *to, int2 q, float4 a, float4 b, const Scale &s) {
+    const uint32_t lo = s.plain ? pack_codes(a, s.inv) : 0u, hi = s.plain ? pack_codes(b, s.inv) : 0u;
+    if (q.y == q.x + 4)
+        *reinterpret_cast<uint2 *>(to + q.x) = make_uint2(lo, hi);
+    else {
+        *reinterpret_cast<uint32_t *>(to + q.x) = lo;
+        *reinterpret_cast<uint32_t *>(to + q.y) = hi;
+    }
+}
+__device__ __forceinline__ uint32_t again(uint32_t w, float ratio) {
+    return pack_codes(make_float4((float)(int8_t)w, (float)(int8_t)(w >> 8), (float)(int8_t)(w >> 16), (float)(int8_t)(w >> 24)), ratio);
+}
+// A block's codes outside the rows s0 .. s1 - 1, re-rounded by `n` threads
+// that each have four words of 16 on their way.
+__device__ __forceinline__ void round_again(int8_t *codes, int page, int dim, int s0, int s1, float ratio, int tid, int n) {
+    uint4 *kept = reinterpret_cast<uint4 *>(codes);
+    const int before = s0 * dim / 16, gap = (s1 - s0) * dim / 16, count = page * dim / 16 - gap;
+    for (int j0 = tid; j0 < count; j0 += 4 * n) {
+        uint4 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int j = j0 + k * n;
+            if (j < count) w[k] = kept[j < before ? j : j + gap];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int j = j0 + k * n;
+            if (j < count)
+                kept[j < before ? j : j + gap] = make_uint4(again(w[k].x, ratio), again(w[k].y, ratio), again(w[k].z, ratio), again(w[k].w, ratio));
+        }
+    }
+}
+
+// Many rows of a sequence. grid: (units, heads, keys or values); unit = one
+// page that a sequence appends to. A thread has one item of every
+// (blockDim / items of a row)-th new row, HELD of them at most, and keeps
+// them in registers: they are read from memory once. Four prompts of 2500 to
+// 8192 tokens, 8 heads of 128, fp32: 57 us, 3.6 TB/s (a CTA for several heads
+// in turn: 69 us; what finding its unit costs, other CTAs' loads cover).
+template <int FT, int HELD>
 __global__ void __launch_bounds__(kThreadsMax)
     kv_append_kernel(const Cache c, const Batch g, const Rope rope, const Rows K, const Rows V) {
     pdl_launch_dependents();
@@ -50,76 +105,146 @@ __global__ void __launch_bounds__(kThreadsMax)
     const int start = s.len - s.n;        // position of the first new token
     const int pg = start / P + u.i;       // page of the sequence
     const int s0 = max(start - pg * P, 0), s1 = min(P, s.len - pg * P);  // its new slots
-    const int id = page_at(g, u.b, pg);
-    if (id < 0) return;
+    const int id = g.table[(int64_t)u.b * g.max_pages + pg];
     const int h = blockIdx.y;
     const bool is_v = blockIdx.z != 0;
+
+    // the block's new values
+    const Rows X = is_v ? V : K;
+    const Rope r = is_v ? Rope{nullptr, 0, 0} : rope;
+    const int per_row = D / 8, step = blockDim.x / per_row, row = threadIdx.x / per_row, j = threadIdx.x - row * per_row;
+    const int2 q = quad_at(r, j);
+    const int pos = pg * P + s0 + row, rows = s1 - s0 - row;  // this thread's: row, row + step, ... of them
+    const int64_t at = (int64_t)(s.row0 + pos - start) * X.stride + (int64_t)h * D;
+    float4 a[HELD], b[HELD];
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) {
+        a[k] = b[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (k * step < rows) {
+            a[k] = load4<FT>(X.p, at + k * step * X.stride + q.x);
+            b[k] = load4<FT>(X.p, at + k * step * X.stride + q.y);
+        }
+    }
+    if (id < 0 || id >= g.num_pages) {
+        if (threadIdx.x == 0) atomicOr(g.err, kDevErrRange);
+        return;
+    }
     const int64_t block = (int64_t)id * c.heads + h;
     int8_t *codes = (is_v ? c.v : c.k) + block * P * D;
     float *scale = (is_v ? c.vs : c.ks) + block;
     const float d_old = s0 > 0 ? *scale : 0.0f;
-
-    // the block's new values, rotated
-    const Rows X = is_v ? V : K;
-    const Rope r = is_v ? Rope{nullptr, 0, 0} : rope;
-    const int per_row = D / 8, items = (s1 - s0) * per_row;
-    float4 a[kItems], b[kItems];
     uint32_t most = 0;
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-        const int i = threadIdx.x + k * blockDim.x;
-        if (i < items) {
-            const int row = i / per_row, j = i - row * per_row;
-            const int2 q = quad_at(r, j);
-            const int64_t pos = (int64_t)pg * P + s0 + row;
-            const int64_t at = (s.row0 + (pos - start)) * X.stride + (int64_t)h * D;
-            a[k] = load4<FT>(X.p, at + q.x);
-            b[k] = load4<FT>(X.p, at + q.y);
-            rotate_item(r, j, pos, a[k], b[k]);
-            most = max_bits(max_bits(most, a[k]), b[k]);
-        }
+    for (int k = 0; k < HELD; ++k) {
+        if (k * step < rows) rotate_item(r, j, pos + k * step, a[k], b[k]);
+        most = max_bits(max_bits(most, a[k]), b[k]);
     }
     __shared__ uint32_t warp_most[kThreadsMax / 32];
     most = __reduce_max_sync(0xffffffffu, most);
     if ((threadIdx.x & 31) == 0) warp_most[threadIdx.x >> 5] = most;
     __syncthreads();
     for (int w = 0; w < (int)blockDim.x / 32; ++w) most = max(most, warp_most[w]);
-
-    const float inf = __int_as_float(0x7F800000);
-    float d = most >= 0x7F800000u ? inf : __fdiv_rn(__uint_as_float(most), 127.0f);
-    if (d < 1.17549435e-38f) d = 0.0f;  // 1 / d would overflow
-    const bool grew = d > d_old;
-    if (!grew) d = d_old;
-    const bool plain = d > 0.0f && d < inf;
-    const float inv = plain ? __fdiv_rn(1.0f, d) : 0.0f;
+    const Scale d = scale_of(most, d_old);
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-        const int i = threadIdx.x + k * blockDim.x;
-        if (i < items) {
-            const int row = i / per_row, j = i - row * per_row;
-            const int2 q = quad_at(r, j);
-            int8_t *to = codes + (s0 + row) * D;
-            *reinterpret_cast<uint32_t *>(to + q.x) = plain ? pack_codes(a[k], inv) : 0u;
-            *reinterpret_cast<uint32_t *>(to + q.y) = plain ? pack_codes(b[k], inv) : 0u;
-        }
-    }
-    if (grew && d_old > 0.0f) {  // the block's other codes, at the new scale
-        const float ratio = plain ? __fdiv_rn(d_old, d) : 0.0f;
-        uint32_t *kept = reinterpret_cast<uint32_t *>(codes);
-        const int words = D / 4, gap = (s1 - s0) * words;
-        for (int j = threadIdx.x; j < P * words - gap; j += blockDim.x) {
-            const int i = j < s0 * words ? j : j + gap;
-            const uint32_t w = kept[i];
-            kept[i] = pack_codes(make_float4((float)(int8_t)w, (float)(int8_t)(w >> 8), (float)(int8_t)(w >> 16),
-                                             (float)(int8_t)(w >> 24)), ratio);
-        }
-    }
-    if (threadIdx.x == 0) *scale = d;
+    for (int k = 0; k < HELD; ++k)
+        if (k * step < rows) store_item(codes + (s0 + row + k * step) * D, q, a[k], b[k], d);
+    if (d.grew && d_old > 0.0f) round_again(codes, P, D, s0, s1, d.plain ? __fdiv_rn(d_old, d.d) : 0.0f, threadIdx.x, blockDim.x);
+    if (threadIdx.x == 0) *scale = d.d;
 }
 
-// grid: (pages, heads, keys or values); each thread 16 codes at a time.
+// The sequence that holds row t: sequence t where each before it has one row,
+// as in a decode step, else found by one warp, 32 sequences at a time.
+// Sequences that do not fit the arrays have no rows.
+__device__ __forceinline__ int sequence_of_row(const Batch &g, int t, int page, Seq &s) {
+    if (t < g.batch) {
+        s = seq_at(g, t, page);
+        if (s.n > 0 && s.row0 == t) return t;
+    }
+    const int lane = threadIdx.x & 31;
+    for (int b0 = 0; b0 < g.batch; b0 += 32) {
+        s.row0 = s.n = s.len = 0;
+        if (b0 + lane < g.batch) s = seq_at(g, b0 + lane, page);
+        const unsigned here = __ballot_sync(0xffffffffu, t >= s.row0 && t - s.row0 < s.n);
+        if (here) {
+            const int l = __ffs(here) - 1;
+            s.row0 = __shfl_sync(0xffffffffu, s.row0, l);
+            s.n = __shfl_sync(0xffffffffu, s.n, l);
+            s.len = __shfl_sync(0xffffffffu, s.len, l);
+            return b0 + l;
+        }
+    }
+    return -1;
+}
+
+// Few rows of a sequence, as in a decode step. grid: (rows, groups of blocks);
+// a warp for each page of a head that a row is the first new one of. It keeps
+// the first new rows that its lanes cover in registers and reads any others
+// twice. 256 sequences of one row, 8 heads of 128, f16: 3.8 us (the kernel for
+// many rows: 15 us).
+constexpr int kRowWarps = 4;
 template <int FT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kRowWarps * 32)
+    kv_append_rows_kernel(const Cache c, const Batch g, const Rope rope, const Rows K, const Rows V) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int P = c.page, D = c.dim, lane = threadIdx.x & 31;
+    const int of = blockIdx.y * kRowWarps + (threadIdx.x >> 5), h = of >> 1;
+    if (h >= c.heads) return;
+    const bool is_v = of & 1;
+    const int t = blockIdx.x;
+    Seq s;
+    const int seq = sequence_of_row(g, t, P, s);
+    if (seq < 0) return;
+    const int pos = s.len - s.n + t - s.row0, pg = pos / P, s0 = pos - pg * P;
+    if (t != s.row0 && s0 != 0) return;  // an earlier row's warp has this page
+    const int count = min(P - s0, s.len - pos);
+    const int id = g.table[(int64_t)seq * g.max_pages + pg];
+    const Rows X = is_v ? V : K;
+    const Rope r = is_v ? Rope{nullptr, 0, 0} : rope;
+    const int per_row = D / 8, step = 32 / per_row, row = lane / per_row, j = lane - row * per_row;
+    const int2 q = quad_at(r, j);
+    const int64_t at = (int64_t)t * X.stride + (int64_t)h * D;
+    const int rows = row < step ? count : 0;
+    auto item = [&](int i, float4 &a, float4 &b) {
+        a = load4<FT>(X.p, at + i * X.stride + q.x);
+        b = load4<FT>(X.p, at + i * X.stride + q.y);
+        rotate_item(r, j, pos + i, a, b);
+    };
+    float4 a0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b0 = a0;
+    if (row < rows) item(row, a0, b0);
+    if (id < 0 || id >= g.num_pages) {
+        if (lane == 0) atomicOr(g.err, kDevErrRange);
+        return;
+    }
+    const int64_t block = (int64_t)id * c.heads + h;
+    int8_t *codes = (is_v ? c.v : c.k) + block * P * D;
+    float *scale = (is_v ? c.vs : c.ks) + block;
+    const float d_old = s0 > 0 ? *scale : 0.0f;
+    uint32_t most = max_bits(max_bits(0u, a0), b0);
+    for (int i = row + step; i < rows; i += step) {
+        float4 a, b;
+        item(i, a, b);
+        most = max_bits(max_bits(most, a), b);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    const Scale d = scale_of(most, d_old);
+    if (row < rows) store_item(codes + (s0 + row) * D, q, a0, b0, d);
+    for (int i = row + step; i < rows; i += step) {
+        float4 a, b;
+        item(i, a, b);
+        store_item(codes + (s0 + i) * D, q, a, b, d);
+    }
+    if (d.grew && d_old > 0.0f) round_again(codes, P, D, s0, s0 + count, d.plain ? __fdiv_rn(d_old, d.d) : 0.0f, lane, 32);
+    __syncwarp();
+    if (lane == 0) *scale = d.d;
+}
+
+// grid: (pages, heads, keys or values); a thread takes 16 bytes of values at
+// a time, four of them on their way. 20000 tokens of 8 heads of 128 into fp32:
+// 37 us, 5.6 TB/s.
+constexpr int kReadThreads = 256;
+template <int FT>
+__global__ void __launch_bounds__(kReadThreads)
     kv_read_kernel(const Cache c, const int32_t *pages, int64_t num_pages, void *K, void *V, unsigned *err) {
     pdl_launch_dependents();
     pdl_wait();
@@ -128,42 +253,76 @@ __global__ void __launch_bounds__(256)
         if (threadIdx.x == 0) atomicOr(err, kDevErrRange);
         return;
     }
-    const int n = c.page * c.dim;
+    constexpr int kE = FT == QMM_F32 ? 1 : 2;  // words of four codes
+    const int items = c.page * c.dim / (4 * kE);
     const bool is_v = blockIdx.z != 0;
     const int64_t block = (int64_t)id * c.heads + blockIdx.y;
-    const int8_t *codes = (is_v ? c.v : c.k) + block * n;
+    const int8_t *codes = (is_v ? c.v : c.k) + block * c.page * c.dim;
     const float d = (is_v ? c.vs : c.ks)[block];
     void *out = is_v ? V : K;
-    const int64_t to = ((int64_t)blockIdx.x * c.heads + blockIdx.y) * n;
-    for (int i = threadIdx.x; i < n / 16; i += blockDim.x) {
-        const uint4 u = reinterpret_cast<const uint4 *>(codes)[i];
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const int64_t to = ((int64_t)blockIdx.x * c.heads + blockIdx.y) * c.page * c.dim;
+    auto value = [&](uint32_t w) {
+        return make_float4(d * (float)(int8_t)w, d * (float)(int8_t)(w >> 8), d * (float)(int8_t)(w >> 16), d * (float)(int8_t)(w >> 24));
+    };
+    for (int i0 = threadIdx.x; i0 < items; i0 += 4 * blockDim.x) {
+        uint32_t w[4][kE];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            store4<FT>(out, to + 16 * i + 4 * k,
-                       make_float4(d * (float)(int8_t)w[k], d * (float)(int8_t)(w[k] >> 8),
-                                   d * (float)(int8_t)(w[k] >> 16), d * (float)(int8_t)(w[k] >> 24)));
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * blockDim.x;
+            if (i >= items) continue;
+            if constexpr (kE == 1)
+                w[k][0] = reinterpret_cast<const uint32_t *>(codes)[i];
+            else {
+                const uint2 two = reinterpret_cast<const uint2 *>(codes)[i];
+                w[k][0] = two.x;
+                w[k][1] = two.y;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * blockDim.x;
+            if (i >= items) continue;
+            if constexpr (kE == 1)
+                store4<FT>(out, to + 4 * i, value(w[k][0]));
+            else {
+                const float4 x = value(w[k][0]), y = value(w[k][1]);
+                reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + to)[i] =
+                    make_uint4(pack_pair(FT, x.x, x.y), pack_pair(FT, x.z, x.w), pack_pair(FT, y.x, y.y), pack_pair(FT, y.z, y.w));
+            }
+        }
     }
+}
+
+template <int FT>
+cudaError_t launch_append(const Cache &c, const Batch &g, const Rope &r, Rows K, Rows V, cudaStream_t s) {
+    // Pages touched: n rows touch at most (n - 2) / page + 2 pages, one row one.
+    const int64_t seqs = g.T < g.batch ? g.T : g.batch, units = g.T / c.page + 2 * seqs;
+    if (units >= g.T) {  // as many as rows: a sequence has one or two
+        const dim3 grid((unsigned)g.T, (unsigned)((2 * c.heads + kRowWarps - 1) / kRowWarps));
+        return launch(kv_append_rows_kernel<FT>, grid, kRowWarps * 32, 0, s, c, g, r, K, V);
+    }
+    const int per_row = c.dim / 8, held = held_rows(c.page, c.dim);
+    int step = c.page / held;
+    while (step * per_row % 32) ++step;  // whole warps
+    const dim3 grid((unsigned)units, (unsigned)c.heads, 2);
+    return held == 4 ? launch(kv_append_kernel<FT, 4>, grid, step * per_row, 0, s, c, g, r, K, V)
+                     : launch(kv_append_kernel<FT, 8>, grid, step * per_row, 0, s, c, g, r, K, V);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const Cache &c, const Batch &g, const Rope &r, int ft, Rows K, Rows V, cudaStream_t s) {
-    // Pages touched: n rows touch at most (n - 2) / page + 2 pages, one row one.
-    const int64_t seqs = g.T < g.batch ? g.T : g.batch;
-    const int64_t units = g.T / c.page + 2 * seqs < g.T ? g.T / c.page + 2 * seqs : g.T;
-    int threads = c.page * c.dim / (8 * kItems);
-    threads = threads < 64 ? 64 : (threads + 31) / 32 * 32;
-    const dim3 grid((unsigned)units, (unsigned)c.heads, 2);
-    auto kernel = ft == QMM_F32 ? kv_append_kernel<QMM_F32> : ft == QMM_F16 ? kv_append_kernel<QMM_F16> : kv_append_kernel<QMM_BF16>;
-    return launch(kernel, grid, threads, 0, s, c, g, r, K, V);
+    return ft == QMM_F32 ? launch_append<QMM_F32>(c, g, r, K, V, s)
+           : ft == QMM_F16 ? launch_append<QMM_F16>(c, g, r, K, V, s) : launch_append<QMM_BF16>(c, g, r, K, V, s);
 }
 
 cudaError_t launch_kv_read(const Cache &c, const int32_t *pages, int64_t n, int64_t num_pages, int ft, void *K, void *V,
                            unsigned *err, cudaStream_t s) {
     const dim3 grid((unsigned)n, (unsigned)c.heads, 2);
     auto kernel = ft == QMM_F32 ? kv_read_kernel<QMM_F32> : ft == QMM_F16 ? kv_read_kernel<QMM_F16> : kv_read_kernel<QMM_BF16>;
-    return launch(kernel, grid, 128, 0, s, c, pages, num_pages, K, V, err);
+    const int items = c.page * c.dim / (ft == QMM_F32 ? 4 : 8);
+    const int threads = items >= 4 * kReadThreads ? kReadThreads : (items / 4 + 31) / 32 * 32;
+    return launch(kernel, grid, threads, 0, s, c, pages, num_pages, K, V, err);
 }
 
 }  // namespace serving
