@@ -17,6 +17,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kLog2e = 1.44269504088896f;
 constexpr int kTopMax = 32;
+constexpr int kDeep = 4;        // vectors on their way to a thread
+constexpr int kVectorsMax = 128;  // 16-byte vectors with candidates
 constexpr int kFoundMax = 256;  // one for each thread: candidates rank themselves
 static_assert(kFoundMax <= kThreads, "a thread for each candidate");
 constexpr int64_t kVocabMax = (int64_t)1 << 20;
@@ -120,12 +122,14 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
-// A chunk of a row: `n` 16-byte vectors from element `first` on, vector v held
-// by thread v % kThreads; of their elements those in 0 .. V - 1 count.
+// A chunk of a row: `n` 16-byte vectors at `at`, from element `first` on; of
+// their elements those in 0 .. V - 1 count, which are all those of the vectors
+// in0 .. in1 - 1. Of these, thread t holds in0 + t, in0 + t + kThreads, ...;
+// a cut vector in front is thread 0's, one at the end thread kThreads - 1's.
 struct Chunk {
     const char *row;
-    int64_t first, V;
-    int n;
+    const uint4 *at;
+    int first, V, n, in0, in1;
 };
 
 // The chunk's `n` largest keys in falling order by rounds of a CTA-wide
@@ -141,7 +145,7 @@ __device__ __noinline__ void largest_keys_by_rounds(const Chunk c, int n, uint64
             mine = 0;
             for (int v = threadIdx.x; v < c.n; v += kThreads)
                 for (int j = 0; j < kVec; ++j) {
-                    const int64_t e = c.first + (int64_t)v * kVec + j;
+                    const int e = c.first + v * kVec + j;
                     const uint64_t key = e >= 0 && e < c.V ? key_of(load_one<FT>(c.row, e), (uint32_t)e) : 0;
                     if (key < last && key > mine) mine = key;
                 }
@@ -176,11 +180,11 @@ __device__ __noinline__ bool keys_above_and_equal(const Chunk c, int n, float ta
     constexpr int kVec = FT == QMM_F32 ? 4 : 8, kWarps = kThreads / 32;
     __shared__ int equal[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t end = c.first + (int64_t)c.n * kVec;
+    const int end = c.first + c.n * kVec;
     __syncthreads();
     if (threadIdx.x == 0) *count = 0;
     __syncthreads();
-    for (int64_t e = c.first + threadIdx.x; e < end; e += kThreads) {
+    for (int e = c.first + (int)threadIdx.x; e < end; e += kThreads) {
         if (e < 0 || e >= c.V) continue;
         const float x = load_one<FT>(c.row, e);
         if (x > tau) {
@@ -191,8 +195,8 @@ __device__ __noinline__ bool keys_above_and_equal(const Chunk c, int n, float ta
     __syncthreads();
     int all = *count;
     if (all > kFoundMax) return false;
-    for (int64_t e0 = c.first; all < n && e0 < end; e0 += kThreads) {  // a CTA's width at a time
-        const int64_t e = e0 + threadIdx.x;
+    for (int e0 = c.first; all < n && e0 < end; e0 += kThreads) {  // a CTA's width at a time
+        const int e = e0 + (int)threadIdx.x;
         const bool is = e >= 0 && e < c.V && e < end && load_one<FT>(c.row, e) == tau;
         const unsigned in_warp = __ballot_sync(0xffffffffu, is);
         if (lane == 0) equal[warp] = __popc(in_warp);
@@ -217,7 +221,7 @@ __device__ constexpr uint32_t kNone = FT == QMM_F32 ? 0xFF800000u : FT == QMM_F1
 
 // A vector that the row's start or end cuts: -inf for elements outside.
 template <int FT>
-__device__ __noinline__ uint4 cut_vector(const char *row, int64_t e, int64_t V) {
+__device__ __noinline__ uint4 cut_vector(const char *row, int e, int V) {
     uint32_t w[4] = {kNone<FT>, kNone<FT>, kNone<FT>, kNone<FT>};
 #pragma unroll
     for (int k = 0; k < (FT == QMM_F32 ? 4 : 8); ++k) {
@@ -231,12 +235,11 @@ __device__ __noinline__ uint4 cut_vector(const char *row, int64_t e, int64_t V) 
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <int FT>
-__device__ __forceinline__ uint4 load_vector(const Chunk &c, int v) {
-    constexpr int kVec = FT == QMM_F32 ? 4 : 8;
-    const int64_t e = c.first + (int64_t)v * kVec;
-    if (e >= 0 && e + kVec <= c.V) return *reinterpret_cast<const uint4 *>(c.row + e * (16 / kVec));
-    return cut_vector<FT>(c.row, e, c.V);
+// The cut vector of this thread, or -1.
+__device__ __forceinline__ int cut_of(const Chunk &c) {
+    if (threadIdx.x == 0 && c.in0) return 0;
+    if (threadIdx.x == kThreads - 1 && c.in1 < c.n && c.n > c.in0) return c.n - 1;
+    return -1;
 }
 
 // The larger of two words, element by element; NaN passed over.
@@ -259,7 +262,7 @@ __device__ __forceinline__ float2 word_values(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// grid: rows x chunks. stats [row][chunk] and keys [row][chunk][top] where a
+// grid: (rows, chunks of `step` vectors). stats [row][chunk] and keys [row][chunk][top] where a
 // row has several chunks.
 //
 // The chunk is read twice, the second time from L1, rather than held in
@@ -270,50 +273,63 @@ __device__ __forceinline__ float2 word_values(uint32_t w) {
 // Its largest keys: the W warps whose threads all hold elements give tau, the
 // smallest of their ceil(top / W)-th largest thread maxima. At least `top`
 // elements reach it, and few more do (top <= 8: 8 warps' smallest maximum,
-// about the 22nd largest element); they are collected while the exponentials
-// are summed, and rank themselves by counting. Where more reach tau than fit,
+// about the 22nd largest element); their vectors are noted while the
+// exponentials are summed, and the elements rank themselves by counting. Where more reach tau than fit,
 // or there is a NaN, the functions above take over.
 template <int FT>
-__global__ void __launch_bounds__(kThreads, 6) logprobs_chunk_kernel(const Logprobs a, int chunks, Stats *stats, uint64_t *keys) {
+__global__ void __launch_bounds__(kThreads, 6) logprobs_chunk_kernel(const Logprobs a, int chunks, int step, Stats *stats, uint64_t *keys) {
     constexpr int kVec = FT == QMM_F32 ? 4 : 8, kWarps = kThreads / 32;
     __shared__ float red[3][kWarps], warp_tau[kWarps];
     __shared__ uint64_t best_of[2][kWarps];
     __shared__ uint64_t found[kFoundMax], top[kTopMax];
-    __shared__ int count;
+    __shared__ int count, vectors_found, vector_of[kVectorsMax];
+    __shared__ uint4 vector_at[kVectorsMax];
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t row = blockIdx.x / chunks;
-    const int chunk = (int)(blockIdx.x - row * chunks);
+    const int64_t row = blockIdx.x, at_chunk = row * chunks + blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float inf = __int_as_float(0x7F800000);
 
     // the chunk as 16-byte vectors of the row's aligned addresses
     Chunk c;
     c.row = static_cast<const char *>(a.X) + row * a.stride * (16 / kVec);
-    c.V = a.V;
+    c.V = (int)a.V;
     const int skew = (int)((uintptr_t)c.row % 16) / (16 / kVec);
-    const int64_t vectors = (a.V + skew + kVec - 1) / kVec, v0 = vectors * chunk / chunks;
+    const int vectors = (c.V + skew + kVec - 1) / kVec, v0 = blockIdx.y * step;
     c.first = v0 * kVec - skew;
-    c.n = (int)(vectors * (chunk + 1) / chunks - v0);
+    c.at = reinterpret_cast<const uint4 *>(c.row - skew * (16 / kVec)) + v0;
+    c.n = max(min(step, vectors - v0), 0);
+    c.in0 = c.first < 0;
+    c.in1 = max(c.n - (c.first + c.n * kVec > c.V), c.in0);  // (one vector may be cut at both ends)
+    const int cut = cut_of(c);
+    const uint4 nothing = make_uint4(kNone<FT>, kNone<FT>, kNone<FT>, kNone<FT>);
+    const uint4 edge = cut >= 0 ? cut_vector<FT>(c.row, c.first + cut * kVec, c.V) : nothing;
 
-    uint32_t w_most = kNone<FT>, w_most2 = kNone<FT>;
-#pragma unroll 4
-    for (int v = threadIdx.x; v < c.n; v += kThreads) {
-        const uint4 u = load_vector<FT>(c, v);
-        w_most = word_max<FT>(w_most, word_max<FT>(u.x, u.y));
-        w_most2 = word_max<FT>(w_most2, word_max<FT>(u.z, u.w));
+    uint32_t w_most = word_max<FT>(edge.x, edge.y), w_most2 = word_max<FT>(edge.z, edge.w);
+    for (int v = c.in0 + threadIdx.x; v < c.in1; v += kDeep * kThreads) {
+        uint4 u[kDeep];
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            u[k] = nothing;
+            if (v + k * kThreads < c.in1) u[k] = c.at[v + k * kThreads];
+        }
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            w_most = word_max<FT>(w_most, word_max<FT>(u[k].x, u[k].y));
+            w_most2 = word_max<FT>(w_most2, word_max<FT>(u[k].z, u[k].w));
+        }
     }
     const float2 m2 = word_values<FT>(word_max<FT>(w_most, w_most2));
     const float mine = fmaxf(m2.x, m2.y);
     float most = warp_nth_largest(mine, 1);
-    const int full = min(c.n, kThreads) / 32;  // warps without an empty thread
+    const int full = min(c.in1 - c.in0, kThreads) / 32;  // warps whose threads all hold a vector
     const int nth = full ? (a.top + full - 1) / full : 0;
     const float nth_most = warp < full && nth > 1 ? warp_nth_largest(mine, nth) : most;
     if (lane == 0) {
         red[0][warp] = most;
         warp_tau[warp] = nth_most;
     }
-    if (threadIdx.x == 0) count = 0;
+    if (threadIdx.x == 0) count = vectors_found = 0;
     __syncthreads();
     float tau = inf;
 #pragma unroll
@@ -330,35 +346,36 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_chunk_kernel(const Logpr
     s.m = most == -inf ? 0.0f : most;
     uint64_t l2 = pair(0.0f, 0.0f), t2 = l2;
     const uint64_t minus = pair(-s.m, -s.m), log2e = pair(kLog2e, kLog2e);
-#pragma unroll 1
-    for (int v = threadIdx.x; v < c.n; v += kThreads) {
-        const uint4 u = load_vector<FT>(c, v);
+    auto add = [&](uint4 u, int v) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        float x[kVec], reach = -inf;
+        float reach = -inf;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 f = word_values<FT>(w[k]);
-            x[FT == QMM_F32 ? k : (2 * k) % kVec] = f.x;
-            if (FT != QMM_F32) x[(2 * k + 1) % kVec] = f.y;
-        }
-#pragma unroll
-        for (int k = 0; k < kVec; k += 2) {
-            const uint64_t d = mul2(add2(pair(x[k], x[k + 1]), minus), log2e);
+        for (int k = 0; k < 4; k += FT == QMM_F32 ? 2 : 1) {
+            const float2 x = FT == QMM_F32 ? make_float2(__uint_as_float(w[k]), __uint_as_float(w[(k + 1) % 4])) : word_values<FT>(w[k]);
+            const uint64_t d = mul2(add2(pair(x.x, x.y), minus), log2e);
             const float2 f = unpair(d);
             const uint64_t e = pair(ex2(f.x), ex2(f.y));
             l2 = add2(l2, e);
             t2 = fma2(e, pair(fmaxf(f.x, -1000.0f), fmaxf(f.y, -1000.0f)), t2);  // 0, not 0 * -inf, where x = -inf
-            reach = max3(reach, x[k], x[k + 1]);
+            reach = max3(reach, x.x, x.y);
         }
         if (reach >= tau) {
-#pragma unroll
-            for (int k = 0; k < kVec; ++k)
-                if (x[k] >= tau) {
-                    const int at = atomicAdd(&count, 1);
-                    // the value and its place in the chunk; the key below
-                    if (at < kFoundMax) found[at] = (uint64_t)__float_as_uint(x[k]) << 32 | (uint32_t)(v * kVec + k);
-                }
+            const int at = atomicAdd(&vectors_found, 1);
+            if (at < kVectorsMax) {
+                vector_at[at] = u;
+                vector_of[at] = v;
+            }
         }
+    };
+    if (cut >= 0) add(edge, cut);
+    const uint4 *at = c.at + c.in0 + threadIdx.x;
+    const uint4 *const end = c.at + c.in1;
+    uint4 u = at < end ? *at : nothing;
+    for (int v = c.in0 + threadIdx.x; v < c.in1; v += kThreads) {
+        const uint4 now = u;
+        at += kThreads;
+        if (at < end) u = *at;  // while this one is added
+        add(now, v);
     }
     s.l = unpair(l2).x + unpair(l2).y;
     s.t = unpair(t2).x + unpair(t2).y;
@@ -379,29 +396,32 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_chunk_kernel(const Logpr
         s.t += red[2][w];
     }
 
-    uint64_t *to = chunks == 1 ? top : keys + (int64_t)blockIdx.x * a.top;
-    if (threadIdx.x == 0 && chunks > 1) stats[blockIdx.x] = s;
+    uint64_t *to = chunks == 1 ? top : keys + at_chunk * a.top;
+    if (threadIdx.x == 0 && chunks > 1) stats[at_chunk] = s;
     if (a.top) {
-        const bool listed = count > kFoundMax;  // by the other function, as keys
+        // the elements of the vectors that reach tau
+        const int vectors_all = vectors_found;
+        for (int i = threadIdx.x; i < min(vectors_all, kVectorsMax) * kVec; i += kThreads) {
+            const int e = c.first + vector_of[i / kVec] * kVec + i % kVec;
+            const float x = load_one<FT>(vector_at, i);
+            if (x >= tau && e >= 0 && e < c.V) {
+                const int n = atomicAdd(&count, 1);
+                if (n < kFoundMax) found[n] = key_of(x, (uint32_t)e);
+            }
+        }
+        __syncthreads();
+        const bool many = vectors_all > kVectorsMax || count > kFoundMax;
         // a NaN, which the maxima pass over, shows in the sum
-        if (s.l != s.l || (listed && !keys_above_and_equal<FT>(c, a.top, tau, found, &count))) {
+        if (s.l != s.l || (many && !keys_above_and_equal<FT>(c, a.top, tau, found, &count))) {
             largest_keys_by_rounds<FT>(c, a.top, to, best_of);
         } else {
             const int all = count;
-            uint64_t key = 0;
-            if ((int)threadIdx.x < all) {
-                key = found[threadIdx.x];
-                if (!listed) {  // -inf elements outside the row, where tau is -inf, have no key
-                    const int64_t e = c.first + (uint32_t)key;
-                    key = e >= 0 && e < a.V ? key_of(__uint_as_float((uint32_t)(key >> 32)), (uint32_t)e) : 0;
-                }
-            }
-            __syncthreads();
-            if ((int)threadIdx.x < all) found[threadIdx.x] = key;
+            const uint64_t key = (int)threadIdx.x < all ? found[threadIdx.x] : 0;
             if ((int)threadIdx.x < a.top) to[threadIdx.x] = 0;  // of a chunk of fewer elements
             __syncthreads();
             int before = 0;
             if (key) {
+#pragma unroll 8
                 for (int i = 0; i < all; ++i) before += found[i] > key;
                 if (before < a.top) to[before] = key;
             }
@@ -486,7 +506,10 @@ template <int FT>
 cudaError_t launch_typed(const Logprobs &a, int chunks, void *ws, cudaStream_t s) {
     Stats *stats = static_cast<Stats *>(ws);
     uint64_t *keys = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + align_up((size_t)a.M * chunks * sizeof(Stats), 16));
-    const cudaError_t e = launch(logprobs_chunk_kernel<FT>, dim3((unsigned)(a.M * chunks)), kThreads, 0, s, a, chunks, stats, keys);
+    constexpr int kVec = FT == QMM_F32 ? 4 : 8;
+    const int vectors = (int)((a.V + 2 * (kVec - 1)) / kVec);  // at most, wherever the row starts
+    const cudaError_t e = launch(logprobs_chunk_kernel<FT>, dim3((unsigned)a.M, (unsigned)chunks), kThreads, 0, s, a, chunks,
+                                 (vectors + chunks - 1) / chunks, stats, keys);
     if (e != cudaSuccess || chunks == 1) return e;
     return launch(logprobs_join_kernel<FT>, dim3((unsigned)a.M), 64, (size_t)chunks * a.top * 8, s, a, chunks, (const Stats *)stats, (const uint64_t *)keys);
 }
