@@ -1,0 +1,129 @@
+"""Serve prompts on a small random decoder: Q4_K projections, a paged 8-bit
+cache of keys and values, attention over it, and log probabilities.
+
+    python examples/serve.py [--layers 4] [--steps 32]
+
+Each step runs a batch in which every sequence brings as many tokens as it
+has (a whole prompt, then one at a time). A layer is
+
+    q, k, v = W_q x, W_k x, W_v x        qmm_mul_mat_multi
+    cache  += rotate(k), v               qmm_kv_append
+    x      += W_o attention(rotate(q))   qmm_kv_attention, qmm_mul_mat
+
+and the last row of each sequence gives its next token and the most likely
+alternatives (qmm_mul_mat, qmm_logprobs)."""
+import argparse
+import os
+import sys
+import time
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+import block_quantized_matmul_q4_gb300 as qmm  # noqa: E402
+
+Q4_K = qmm.QMM_TYPE_Q4_K
+
+
+class Linear:
+    """Packed Q4_K weights [N][K]."""
+
+    def __init__(self, N, K, generator):
+        w = torch.randn(N, K, generator=generator, device="cuda") * K ** -0.5
+        blocks = qmm.empty_blocks(Q4_K, N, K)
+        qmm.qmm_quantize_weights(Q4_K, w, blocks, N, K)
+        self.N, self.K, self.packed = N, K, qmm.empty_packed(Q4_K, N, K)
+        qmm.qmm_repack_weights(Q4_K, blocks, self.packed, N, K)
+
+    def __call__(self, x):
+        y = torch.empty(x.size(0), self.N, device="cuda")
+        qmm.qmm_mul_mat(Q4_K, self.packed, self.N, self.K, x, x.size(0), y)
+        return y
+
+
+class Server:
+    def __init__(self, layers=4, hidden=1024, q_heads=16, heads=4, dim=64, vocab=32000, pages=512, page=32, positions=4096, seed=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.hidden, self.q_heads, self.heads, self.dim, self.page = hidden, q_heads, heads, dim, page
+        self.embedding = torch.randn(vocab, hidden, generator=g, device="cuda")
+        self.qkv = [[Linear(n * dim, hidden, g) for n in (q_heads, heads, heads)] for _ in range(layers)]
+        self.out = [Linear(hidden, q_heads * dim, g) for _ in range(layers)]
+        self.head = Linear(vocab, hidden, g)
+        self.caches = [qmm.empty_kv_cache(pages, heads, page, dim) for _ in range(layers)]  # one page table for all
+        f = 10000.0 ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)
+        a = torch.arange(positions, dtype=torch.float64)[:, None] * f
+        self.rope = qmm.Rope(torch.stack((a.cos(), a.sin()), -1).float().cuda())
+        self.free = list(range(pages))
+        self.most_pages = -(-positions // page)
+        self.tables, self.lengths = [], []
+
+    def add(self):
+        """A new sequence; its number."""
+        self.tables.append([])
+        self.lengths.append(0)
+        return len(self.lengths) - 1
+
+    def step(self, seqs, tokens, top=5):
+        """tokens[i]: the new tokens of sequence seqs[i]. Returns the logits of each sequence's last row, the most
+        likely ids [len(seqs)][top] and their log probabilities."""
+        first = [0]
+        for s, t in zip(seqs, tokens):
+            first.append(first[-1] + len(t))
+            self.lengths[s] += len(t)
+            while len(self.tables[s]) * self.page < self.lengths[s]:
+                self.tables[s].append(self.free.pop())
+        table = torch.zeros(len(seqs), self.most_pages, dtype=torch.int32)
+        for i, s in enumerate(seqs):
+            table[i, :len(self.tables[s])] = torch.tensor(self.tables[s], dtype=torch.int32)
+        length = torch.tensor([self.lengths[s] for s in seqs], dtype=torch.int32)
+        batch = qmm.KvBatch(table.cuda(), torch.tensor(first, dtype=torch.int32).cuda(), length.cuda())
+        max_q, max_kv = max(len(t) for t in tokens), int(length.max())
+
+        T = first[-1]
+        x = self.embedding[torch.tensor([t for ts in tokens for t in ts]).cuda()]
+        for qkv, out, cache in zip(self.qkv, self.out, self.caches):
+            q, k, v = (torch.empty(T, w.N, device="cuda") for w in qkv)
+            normed = torch.nn.functional.rms_norm(x, (self.hidden,))
+            qmm.qmm_mul_mat_multi(Q4_K, [w.packed for w in qkv], [w.N for w in qkv], self.hidden, normed, T, [q, k, v])
+            qmm.qmm_kv_append(cache, batch, self.rope, k.view(T, self.heads, self.dim), v.view(T, self.heads, self.dim))
+            q = q.view(T, self.q_heads, self.dim)
+            mixed = torch.empty_like(q)
+            qmm.qmm_kv_attention(cache, batch, self.rope, q, mixed, scale=self.dim ** -0.5, max_q=max_q, max_kv=max_kv)
+            x = x + out(mixed.view(T, -1))
+        last = torch.nn.functional.rms_norm(x[torch.tensor(first[1:]).cuda() - 1], (self.hidden,))
+        logits = self.head(last)
+        ids = torch.empty(len(seqs), top, dtype=torch.int32, device="cuda")
+        logp = torch.empty(len(seqs), top, device="cuda")
+        qmm.qmm_logprobs(logits, top_ids=ids, top_logp=logp)
+        qmm.qmm_check_device_error()
+        return logits, ids, logp
+
+
+def main():
+    p = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
+    p.add_argument("--layers", type=int, default=4)
+    p.add_argument("--steps", type=int, default=32)
+    a = p.parse_args()
+    server = Server(layers=a.layers)
+    g = torch.Generator().manual_seed(1)
+    prompts = [torch.randint(0, 32000, (n,), generator=g).tolist() for n in (700, 33, 1, 256)]
+    seqs = [server.add() for _ in prompts]
+    logits, ids, logp = server.step(seqs, prompts)
+    made = [[] for _ in seqs]
+    total = torch.zeros(len(seqs))
+    start = time.perf_counter()
+    for _ in range(a.steps):
+        picked = ids[:, 0].tolist()
+        total += logp[:, 0].cpu()
+        for m, t in zip(made, picked):
+            m.append(t)
+        logits, ids, logp = server.step(seqs, [[t] for t in picked])
+    seconds = time.perf_counter() - start
+    for s, m, lp in zip(seqs, made, total.tolist()):
+        print(f"sequence {s}: {server.lengths[s]} tokens, log probability of the {len(m)} new ones {lp:.2f}: {m[:8]}")
+    if a.steps:
+        print(f"{seconds / a.steps * 1e3:.2f} ms a step of {len(seqs)} sequences")
+
+
+if __name__ == "__main__":
+    main()
