@@ -22,8 +22,8 @@ constexpr int kVectorsMax = 128;  // 16-byte vectors with candidates
 constexpr int kFoundMax = 256;  // one for each thread: candidates rank themselves
 static_assert(kFoundMax <= kThreads, "a thread for each candidate");
 constexpr int64_t kVocabMax = (int64_t)1 << 20;
-constexpr int kChunkLarge = 32768, kChunkSmall = 8192;  // bytes (see chunks_of)
-constexpr int kListsMax = 160, kSmallChunksMax = 128;    // chunks of a row
+constexpr int kChunkLarge = 102400, kChunkSmall = 8192;  // bytes (see chunks_of)
+constexpr int kListsMax = 128;                           // chunks of a row
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -265,10 +265,10 @@ __device__ __forceinline__ float2 word_values(uint32_t w) {
 // grid: (rows, chunks of `step` vectors). stats [row][chunk] and keys [row][chunk][top] where a
 // row has several chunks.
 //
-// The chunk is read twice, the second time from L1, rather than held in
+// The chunk is read twice, the second time from L1 or L2, rather than held in
 // registers: 48 warps an SM instead of 24 hide the loads, and the code stays
-// within the instruction cache (unrolled over 64 registers: 280 us for 4096 x
-// 50001 bf16, a third of it waiting for instructions).
+// within the instruction cache (32 KB unrolled over 64 registers: 280 us for
+// 4096 x 50001 bf16, a third of it waiting for instructions; 147 so).
 //
 // Its largest keys: the W warps whose threads all hold elements give tau, the
 // smallest of their ceil(top / W)-th largest thread maxima. At least `top`
@@ -492,14 +492,20 @@ __global__ void __launch_bounds__(64) logprobs_join_kernel(const Logprobs a, int
     finish_row<FT>(a, row, s, top);
 }
 
-// Chunks of a row: of about 32 KB, which six CTAs hold in an SM's L1, or of 8
-// KB where those would leave SMs idle, as long as the join can hold their lists.
+// Chunks of a row: of up to 100 KB, as each has its maximum, threshold and
+// ranking to find beside its elements (4096 rows of 50001 bf16 and their 8
+// largest: 102 us in one chunk, 120 in two, 147 in four, although only the
+// last are read again from L1). Where those would give an SM
+// fewer than three CTAs they are cut down to 8 KB (64 rows of 131073 fp32:
+// 15.9 us in 16 chunks, 13.5 in 8).
 int chunks_of(int64_t M, int64_t V, int size) {
-    auto chunks = [&](int bytes) { return (int)((V * size + 15 + bytes - 1) / bytes); };
-    if (M * chunks(kChunkLarge) < 2 * kSms && chunks(kChunkSmall) <= kSmallChunksMax) return chunks(kChunkSmall);
-    return chunks(kChunkLarge);
+    auto chunks = [&](int bytes) { return (V * size + 15 + bytes - 1) / bytes; };
+    const int64_t large = chunks(kChunkLarge), want = (3 * kSms + M - 1) / M;
+    const int64_t most = chunks(kChunkSmall) < kListsMax ? chunks(kChunkSmall) : kListsMax;
+    const int64_t cut = want < most ? want : most;
+    return (int)(cut > large ? cut : large);
 }
-static_assert((kVocabMax * 4 + 15) / kChunkLarge + 1 <= kListsMax && kSmallChunksMax <= kListsMax, "join's lists");
+static_assert((kVocabMax * 4 + 15) / kChunkLarge + 1 <= kListsMax, "join's lists");
 static_assert(kListsMax * kTopMax * 8 <= 48 * 1024, "join's shared memory");
 
 template <int FT>
