@@ -26,7 +26,10 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kStep = 16;        // tokens of a warp's step: one MMA tile of the cache
-constexpr int kAhead = 2;        // steps between a prefetch and its use
+// Steps between a prefetch and its use (131071 tokens, 8 heads of 128: 68 us
+// with one, 70 with two, 76 with four; a ring of bulk copies into shared
+// memory in place of prefetches and loads: 70 to 85).
+constexpr int kAhead = 1;
 constexpr int kPageBlock = 256;  // pages whose ids and scales are staged at once
 static_assert(kSplitTokens == kWarps * kStep, "a round of the warps' steps");
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -461,8 +464,10 @@ constexpr int64_t kFewRows = 64;
 // us, 149 with a second kernel).
 constexpr int kClusterMax = 8;
 constexpr int64_t kClusterTokens = 4096;  // up to which more splits are not worth a second launch
-bool joins_in_cluster(const Plan &p, int64_t tiles) {
-    return p.tile_rows != kPrefillRows && p.splits > 1 && p.splits <= kClusterMax && tiles * p.splits <= 4 * kSms;
+// CTAs of few rows that an SM holds, as their registers allow.
+int at_once(int tile_rows, int dim) { return tile_rows == 8 && dim <= 128 ? 4 : 2; }
+bool joins_in_cluster(const Plan &p, int dim, int64_t tiles) {
+    return p.tile_rows != kPrefillRows && p.splits > 1 && p.splits <= kClusterMax && tiles * p.splits <= at_once(p.tile_rows, dim) * kSms;
 }
 Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv, int64_t window,
              int ft) {
@@ -477,10 +482,12 @@ Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_
     const int64_t tiles = (T * group + p.tile_rows - 1) / p.tile_rows;  // about as many have rows
     int64_t kv = max_kv < 1 ? 1 : max_kv;
     if (window && window + max_q < kv) kv = window + max_q;
-    // CTAs for every SM to hold four and two waves of them; where there are many
-    // anyway (ragged lengths), four waves, so that they even out.
+    // A single sequence: as many CTAs as run at once (131071 tokens, 8 heads of
+    // 128: 60 us, two waves 68). Several of different lengths: two waves of the
+    // longest's splits, four where there are many CTAs anyway, so that they
+    // even out (8 sequences of up to 32768: 90 us, one wave 98).
     const int64_t ctas = tiles * heads > 0 ? tiles * heads : 1;
-    const int64_t want = (ctas < kSms || p.tile_rows == kPrefillRows ? 8 : 16) * kSms / ctas;
+    const int64_t want = (p.tile_rows == kPrefillRows ? 8 : at_once(p.tile_rows, dim) * (seqs == 1 ? 1 : ctas < kSms ? 2 : 4)) * kSms / ctas;
     int64_t splits = want < 1 ? 1 : want;
     const int64_t most = (kv + kSplitTokens - 1) / kSplitTokens;
     if (splits > most) splits = most;
@@ -493,7 +500,7 @@ Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_
     }
     p.chunk = (int)(((kv + splits - 1) / splits + kSplitTokens - 1) / kSplitTokens * kSplitTokens);
     p.splits = (int)((kv + p.chunk - 1) / p.chunk);
-    p.cluster = joins_in_cluster(p, ctas);
+    p.cluster = joins_in_cluster(p, dim, ctas);
     return p;
 }
 
