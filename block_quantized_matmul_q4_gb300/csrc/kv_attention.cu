@@ -466,8 +466,8 @@ constexpr int kClusterMax = 8;
 constexpr int64_t kClusterTokens = 4096;  // up to which more splits are not worth a second launch
 // CTAs of few rows that an SM holds, as their registers allow.
 int at_once(int tile_rows, int dim) { return tile_rows == 8 && dim <= 128 ? 4 : 2; }
-bool joins_in_cluster(const Plan &p, int dim, int64_t tiles) {
-    return p.tile_rows != kPrefillRows && p.splits > 1 && p.splits <= kClusterMax && tiles * p.splits <= at_once(p.tile_rows, dim) * kSms;
+bool joins_in_cluster(int tile_rows, int splits, int dim, int64_t tiles) {
+    return tile_rows != kPrefillRows && splits > 1 && splits <= kClusterMax && tiles * splits <= at_once(tile_rows, dim) * kSms;
 }
 Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv, int64_t window,
              int ft) {
@@ -498,9 +498,11 @@ Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_
         const int64_t sum = ft == QMM_F32 ? kSumTokens : kSumTokens16;
         if (splits < (kv + sum - 1) / sum) splits = (kv + sum - 1) / sum;
     }
+    p.most = (int)splits;
     p.chunk = (int)(((kv + splits - 1) / splits + kSplitTokens - 1) / kSplitTokens * kSplitTokens);
     p.splits = (int)((kv + p.chunk - 1) / p.chunk);
-    p.cluster = joins_in_cluster(p, dim, ctas);
+    p.cluster = joins_in_cluster(p.tile_rows, p.splits, dim, ctas);
+    p.no_parts = p.most == 1 || joins_in_cluster(p.tile_rows, p.most, dim, ctas);
     return p;
 }
 
@@ -523,11 +525,12 @@ cudaError_t launch_tiles(const Cache &c, const Batch &g, const Rope &r, const At
 
 size_t kv_attention_bytes(int heads, int dim, int page, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv) {
     (void)page;
-    // for any window: a window only lowers the number of splits' tokens, not their bound
+    // For any window: one acts like a smaller max_kv, which never has a larger
+    // `most`, although it may round to more splits.
     size_t most = 0;
     for (const int ft : {QMM_F32, QMM_F16}) {
         const Plan p = plan_of(heads, dim, batch, q_heads, T, max_q, max_kv, 0, ft);
-        const size_t bytes = p.splits == 1 || p.cluster ? 0 : (size_t)p.units * heads * p.splits * p.tile_rows * (dim + 4) * 4;
+        const size_t bytes = p.no_parts ? 0 : (size_t)p.units * heads * p.most * p.tile_rows * (dim + 4) * 4;
         if (bytes > most) most = bytes;
     }
     return most;

@@ -104,7 +104,8 @@ struct Plan {
     int tile_rows;
     int64_t units;
     int chunk, splits;
-    bool cluster;
+    int most;       // splits before a chunk is rounded up, which may leave fewer
+    bool cluster, no_parts;  // no_parts: nor with any fewer splits
 };
 constexpr int kSplitTokens = 64;  // splits begin at multiples of this
 constexpr int kPrefillRows = 128;

@@ -111,3 +111,13 @@ def test_workspace_sizes(lib):
     at = lambda cache, b, h, T, mq, mk: lib.qmm_kv_attention_workspace_bytes(ref(Cache(**cache)), b, h, i64(T), i64(mq), i64(mk))  # noqa: E731
     assert at(CACHE | dict(dim=100), 1, 4, 1, 1, 10) == 0 and at(CACHE, 1, 3, 1, 1, 10) == 0 and at(CACHE, 0, 4, 1, 1, 10) == 0
     assert at(CACHE, 1, 4, 1, 1, 100000) > 0 and at(CACHE, 1, 4, 1, 1, 64) == 0
+
+
+@pytest.mark.parametrize("batch,q_heads,max_q", [(1, 4, 1), (1, 32, 1), (3, 8, 1), (7, 16, 200), (64, 4, 1), (2, 4, 90)])
+def test_workspace_holds_a_shorter_cache(lib, batch, q_heads, max_q):
+    """A window makes a call split like one of a shorter cache: the size for a cache is no less than for any shorter one."""
+    i64, most = ctypes.c_int64, 0
+    for kv in list(range(64, 6000, 32)) + list(range(6000, 140000, 992)):
+        need = lib.qmm_kv_attention_workspace_bytes(ref(Cache(**CACHE)), batch, q_heads, i64(batch * max_q), i64(max_q), i64(kv))
+        assert need >= most, kv
+        most = need
