@@ -456,6 +456,11 @@ __global__ void __launch_bounds__(kJoinThreads)
 // Tokens that kv_prefill_wide.cu's tensor cores may sum for an fp32 and for a
 // 16-bit output.
 constexpr int64_t kSumTokens = 512, kSumTokens16 = 8192;
+// Tokens that a prompt's split has at least (8 rows' heads of 128, 2000 tokens:
+// 26 us with 128, 40 with 64), and tokens by which splitting must shorten its
+// walk to be worth the second kernel (2 sequences of up to 600 tokens over
+// 1500, 16 heads of 64, window 512: 23 us in one part, 31 in two).
+constexpr int64_t kPrefillSplit = 128, kJoinTokens = 512;
 // Rows of a sequence up to which a tile is eight or sixteen of them.
 constexpr int64_t kFewRows = 64;
 // Splits of few rows join in a (portable) cluster where all CTAs run at once:
@@ -464,10 +469,13 @@ constexpr int64_t kFewRows = 64;
 // us, 149 with a second kernel).
 constexpr int kClusterMax = 8;
 constexpr int64_t kClusterTokens = 4096;  // up to which more splits are not worth a second launch
-// CTAs of few rows that an SM holds, as their registers allow.
-int at_once(int tile_rows, int dim) { return tile_rows == 8 && dim <= 128 ? 4 : 2; }
-bool joins_in_cluster(int tile_rows, int splits, int dim, int64_t tiles) {
-    return tile_rows != kPrefillRows && splits > 1 && splits <= kClusterMax && tiles * splits <= at_once(tile_rows, dim) * kSms;
+// CTAs that an SM holds, as their registers and tensor memory allow.
+int at_once(int tile_rows, int dim, int ft) {
+    if (tile_rows == kPrefillRows) return ft != QMM_F32 && dim <= 128 ? 2 : 1;
+    return tile_rows == 8 && dim <= 128 ? 4 : 2;
+}
+bool joins_in_cluster(int tile_rows, int splits, int dim, int ft, int64_t tiles) {
+    return tile_rows != kPrefillRows && splits > 1 && splits <= kClusterMax && tiles * splits <= at_once(tile_rows, dim, ft) * kSms;
 }
 Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_q, int64_t max_kv, int64_t window,
              int ft) {
@@ -481,16 +489,23 @@ Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_
     p.units = T * group / p.tile_rows + seqs;
     const int64_t tiles = (T * group + p.tile_rows - 1) / p.tile_rows;  // about as many have rows
     int64_t kv = max_kv < 1 ? 1 : max_kv;
-    if (window && window + max_q < kv) kv = window + max_q;
+    const bool prompts = p.tile_rows == kPrefillRows;
+    if (window) {  // what one tile sees, from a multiple of 16 on
+        const int64_t span = window + 16 + (prompts ? kPrefillRows / group + 1 : max_q);
+        if (span < kv) kv = span;
+    }
     // A single sequence: as many CTAs as run at once (131071 tokens, 8 heads of
     // 128: 60 us, two waves 68). Several of different lengths: two waves of the
     // longest's splits, four where there are many CTAs anyway, so that they
-    // even out (8 sequences of up to 32768: 90 us, one wave 98).
+    // even out (8 sequences of up to 32768: 90 us, one wave 98). Prompts have
+    // tiles enough in most calls and long starts: as many CTAs as run at once
+    // (256 tokens over 8192, 8 heads of 128, fp32: 42 us, two waves 58).
     const int64_t ctas = tiles * heads > 0 ? tiles * heads : 1;
-    const int64_t want = (p.tile_rows == kPrefillRows ? 8 : at_once(p.tile_rows, dim) * (seqs == 1 ? 1 : ctas < kSms ? 2 : 4)) * kSms / ctas;
+    const int64_t want = at_once(p.tile_rows, dim, ft) * (prompts || seqs == 1 ? 1 : ctas < kSms ? 2 : 4) * kSms / ctas;
     int64_t splits = want < 1 ? 1 : want;
-    const int64_t most = (kv + kSplitTokens - 1) / kSplitTokens;
+    const int64_t least = prompts ? kPrefillSplit : kSplitTokens, most = (kv + least - 1) / least;
     if (splits > most) splits = most;
+    if (prompts && kv - kv / splits <= kJoinTokens) splits = 1;
     // a short cache is read sooner than a second kernel starts
     if (p.tile_rows != kPrefillRows && kv <= kClusterTokens && splits > kClusterMax) splits = kClusterMax;
     if (splits > 256) splits = 256;
@@ -501,8 +516,8 @@ Plan plan_of(int heads, int dim, int batch, int q_heads, int64_t T, int64_t max_
     p.most = (int)splits;
     p.chunk = (int)(((kv + splits - 1) / splits + kSplitTokens - 1) / kSplitTokens * kSplitTokens);
     p.splits = (int)((kv + p.chunk - 1) / p.chunk);
-    p.cluster = joins_in_cluster(p.tile_rows, p.splits, dim, ctas);
-    p.no_parts = p.most == 1 || joins_in_cluster(p.tile_rows, p.most, dim, ctas);
+    p.cluster = joins_in_cluster(p.tile_rows, p.splits, dim, ft, ctas);
+    p.no_parts = p.most == 1 || joins_in_cluster(p.tile_rows, p.most, dim, ft, ctas);
     return p;
 }
 
