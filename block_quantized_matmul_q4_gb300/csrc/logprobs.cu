@@ -14,7 +14,7 @@ namespace qmm {
 namespace serving {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kCtas = 6;  // of an SM
 constexpr float kLog2e = 1.44269504088896f;
 constexpr int kTopMax = 32;
 constexpr int kDeep = 4;        // vectors on their way to a thread
@@ -277,7 +277,7 @@ __device__ __forceinline__ float2 word_values(uint32_t w) {
 // exponentials are summed, and the elements rank themselves by counting. Where more reach tau than fit,
 // or there is a NaN, the functions above take over.
 template <int FT>
-__global__ void __launch_bounds__(kThreads, 6) logprobs_chunk_kernel(const Logprobs a, int chunks, int step, Stats *stats, uint64_t *keys) {
+__global__ void __launch_bounds__(kThreads, kCtas) logprobs_chunk_kernel(const Logprobs a, int chunks, int step, Stats *stats, uint64_t *keys) {
     constexpr int kVec = FT == QMM_F32 ? 4 : 8, kWarps = kThreads / 32;
     __shared__ float red[3][kWarps], warp_tau[kWarps];
     __shared__ uint64_t best_of[2][kWarps];
@@ -495,12 +495,12 @@ __global__ void __launch_bounds__(64) logprobs_join_kernel(const Logprobs a, int
 // Chunks of a row: of up to 100 KB, as each has its maximum, threshold and
 // ranking to find beside its elements (4096 rows of 50001 bf16 and their 8
 // largest: 102 us in one chunk, 120 in two, 147 in four, although only the
-// last are read again from L1). Where those would give an SM
-// fewer than three CTAs they are cut down to 8 KB (64 rows of 131073 fp32:
-// 15.9 us in 16 chunks, 13.5 in 8).
+// last are read again from L1). Where those would be fewer than run
+// at once they are cut, down to 8 KB (64 rows of 131073 fp32 from memory: 16.0
+// us in 15 chunks, 19.3 in 8).
 int chunks_of(int64_t M, int64_t V, int size) {
     auto chunks = [&](int bytes) { return (V * size + 15 + bytes - 1) / bytes; };
-    const int64_t large = chunks(kChunkLarge), want = (3 * kSms + M - 1) / M;
+    const int64_t large = chunks(kChunkLarge), want = (kCtas * kSms + M - 1) / M;
     const int64_t most = chunks(kChunkSmall) < kListsMax ? chunks(kChunkSmall) : kListsMax;
     const int64_t cut = want < most ? want : most;
     return (int)(cut > large ? cut : large);
