@@ -267,3 +267,19 @@ def test_long_prompts_agree_with_decode(q, dim, kind, window):  # noqa: F811
     a, b = a.double(), b.double()
     assert ((a - b).abs() <= 2 * (rel * top + EPS[kind] * (b.abs() + rel * top))).all()
     assert ((la - lb).abs() <= 2 * (e + 2.0 ** -20 + 2.0 ** -22 * lb.abs())).all()
+
+
+@pytest.mark.parametrize("seqs,q_heads,dim,kind", [([(1, 5200)], 2, 64, "f32"), ([(1, 9000), (1, 300)], 4, 128, "f16"), ([(90, 5000), (1, 40)], 4, 64, "bf16"),
+                                                   ([(70, 4100)], 2, 192, "f32")])
+def test_nothing_is_written_past_the_workspace(q, seqs, q_heads, dim, kind):  # noqa: F811
+    """Windows change how a call splits: whatever they are, it keeps to the size that was asked for."""
+    c = Case(q, seqs, 2, 32, dim, seed=dim)
+    x = inputs(c, q_heads, kind)
+    max_q, max_kv = max(n for n, _ in seqs), max(m for _, m in seqs)
+    need = q.qmm_kv_attention_workspace_bytes(c.cache, len(seqs), q_heads, c.rows, max_q, max_kv)
+    rows = {0, c.rows // 2, c.rows - 1}
+    for window in (0, 1, 100, 600, 1000, 1700, 2500, 3300, 4500):
+        ws = torch.full((need + (1 << 20),), 0xAB, dtype=torch.uint8, device="cuda")
+        out, lse = call(q, c, x, window=window, workspace=ws, ws_bytes=need)
+        assert bool((ws[need:] == 0xAB).all()), window
+        check(c, x, kind, out, lse, rows=rows, window=window)

@@ -214,3 +214,17 @@ def test_nothing_to_do(q):
     q.qmm_kv_read(c.cache, torch.empty(0, dtype=torch.int32, device="cuda"), empty, empty)
     q.qmm_check_device_error()
     check_append(c)
+
+
+@pytest.mark.parametrize("heads,page,dim,kind,rot", [(3, 16, 128, "f32", 128), (1, 32, 96, "bf16", 32), (2, 128, 256, "f16", 0), (5, 64, 64, "f32", 16),
+                                                     (1, 16, 192, "f16", 192)])
+def test_append_few_rows(q, heads, page, dim, kind, rot):
+    """Many sequences of one or two new rows, some of none, one of many: a warp takes each touched page."""
+    seqs = [(1, 1 + 7 * b) for b in range(30)] + [(0, 5), (2, 2), (0, 0), (2, page + 1), (2, 2 * page), (40, 47 + page)]
+    seqs += [(b % 3, 40 + b) for b in range(40)]
+    c = Case(q, seqs, heads, page, dim, kind, seed=dim + heads)
+    assert c.rows <= 2 * min(len(seqs), c.rows)
+    table = rope_table(c.most * page, rot) if rot else None
+    q.qmm_kv_append(c.cache, c.batch, q.Rope(torch.from_numpy(table).cuda()) if rot else None, *c.dev_x)
+    q.qmm_check_device_error()
+    check_append(c, table)

@@ -126,3 +126,14 @@ def test_outputs_are_optional_and_workspace_is_the_callers(q):
     with pytest.raises(q.QmmError, match="workspace"):
         q.qmm_logprobs(x, given, lse, workspace=ws, ws_bytes=16)
     q.qmm_logprobs(torch.empty(0, 10, device="cuda"))
+
+
+@pytest.mark.parametrize("M,V,kind,top", [(920, 25000, "f32", 8), (920, 26001, "f32", 3), (920, 51301, "bf16", 1), (40, 262147, "f16", 32)])
+def test_large_chunks(q, M, V, kind, top):
+    """Rows of one, two and many chunks, where there are enough rows for large ones."""
+    g = torch.Generator().manual_seed(V)
+    x = (torch.randn(M, V, generator=g) * 3).to(TYPES[kind]).cuda()
+    given = torch.randint(0, V, (M, 1), generator=g, dtype=torch.int32).cuda()
+    got = run(q, x, given, top)
+    rows = list(range(0, M, max(1, M // 12)))
+    check({k: v[rows] for k, v in got.items()}, x[rows], given[rows], top)
